@@ -1,4 +1,4 @@
-"""Thin ctypes binding of libso2conv (include/so2conv.h) for torch tensors.
+"""Thin ctypes binding of libso2conv (include/so2conv.h, so2model.h) for torch tensors.
 
 Argument marshalling only: every step of the convolution runs in the
 library's CUDA kernels.  Torch supplies device memory (inputs, outputs and
@@ -30,6 +30,30 @@ class Desc(ctypes.Structure):
 class Params(ctypes.Structure):
     _fields_ = [("w", ctypes.c_void_p), ("w_rad", ctypes.c_void_p),
                 ("b_rad", ctypes.c_void_p)]
+
+
+class EmbedDesc(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int64), ("channels", ctypes.c_int32),
+                ("n_comp", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("table_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("pad_id", ctypes.c_int64)]
+
+
+class RouteDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("n_experts", "top_k", "n_groups", "top_groups", "group_top", "score",
+                 "renormalise")] + [("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class MixDesc(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("n_weights", ctypes.c_int64), ("expert_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
+
+
+class DropoutDesc(ctypes.Structure):
+    _fields_ = [("channels", ctypes.c_int32), ("n_comp", ctypes.c_int32),
+                ("unit", ctypes.c_int32), ("p", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
 class So2Error(RuntimeError):
@@ -96,6 +120,25 @@ def load():
     lib.so2conv_profile_read.argtypes = [ctypes.c_int, ctypes.POINTER(ctypes.c_int),
                                          ctypes.POINTER(ctypes.c_double)]
     lib.so2conv_profile_read.restype = ctypes.c_int
+    pe, pr, pm, pp = (ctypes.POINTER(c) for c in (EmbedDesc, RouteDesc, MixDesc, DropoutDesc))
+    lib.so2conv_embed_workspace_size.argtypes = [pe, i64, ctypes.c_int]
+    lib.so2conv_embed_workspace_size.restype = sz
+    lib.so2conv_embed_forward.argtypes = [pe, i64, vp, vp, vp, i64, vp, sz, vp]
+    lib.so2conv_embed_forward.restype = ctypes.c_int
+    lib.so2conv_embed_backward.argtypes = [pe, i64, vp, vp, i64, vp, vp, sz, vp]
+    lib.so2conv_embed_backward.restype = ctypes.c_int
+    lib.so2conv_route_forward.argtypes = [pr, i64, vp, vp, vp, vp, vp, vp]
+    lib.so2conv_route_forward.restype = ctypes.c_int
+    lib.so2conv_route_backward.argtypes = [pr, i64, vp, vp, vp, vp, vp]
+    lib.so2conv_route_backward.restype = ctypes.c_int
+    lib.so2conv_mix_workspace_size.argtypes = [pm, i64, ctypes.c_int]
+    lib.so2conv_mix_workspace_size.restype = sz
+    lib.so2conv_mix_experts_forward.argtypes = [pm, i64, vp, vp, vp, vp, vp, sz, vp]
+    lib.so2conv_mix_experts_forward.restype = ctypes.c_int
+    lib.so2conv_mix_experts_backward.argtypes = [pm, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.so2conv_mix_experts_backward.restype = ctypes.c_int
+    lib.so2conv_dropout.argtypes = [pp, i64, vp, vp, vp, vp, vp, vp]
+    lib.so2conv_dropout.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -142,6 +185,7 @@ class Workspace:
 
 
 _WS = {}
+_MODEL_WS = {}  # device -> workspace of the last model operator there, if it came after the others
 
 
 def workspace(device):
@@ -163,8 +207,22 @@ def _wsarg(desc, n_nodes, n_edges, which, device, ws):
     need = workspace_size(desc, n_nodes, n_edges, which)
     if need == 0:
         raise So2Error(2, "workspace_size")
-    w = ws or workspace(device)
-    return w.get(need)
+    return _default_ws(device, ws).get(need)
+
+
+def _default_ws(device, ws):
+    if ws:
+        return ws
+    _MODEL_WS.pop(_device(device), None)
+    return workspace(device)
+
+
+def _device(device):
+    """The device with its index, so that "cuda" and "cuda:0" are one key."""
+    d = torch.device(device)
+    if d.type == "cuda" and d.index is None:
+        return torch.device("cuda", torch.cuda.current_device())
+    return d
 
 
 def forward(desc, x, edge_index, edge_vec, w, w_rad, b_rad, out=None, ws=None):
@@ -253,8 +311,9 @@ def double_backward(desc, x, edge_index, edge_vec, w, w_rad, b_rad, grad_out, gg
 
 
 def check(device, ws=None):
-    """Synchronise and return the device status of the last call (0 = ok)."""
-    w = ws or workspace(device)
+    """Synchronise and return the device status of the last call (0 = ok): the
+    last one made with `ws`, or without a workspace of its own on `device`."""
+    w = ws or _MODEL_WS.get(_device(device)) or workspace(device)
     if w.buf is None:
         return 0
     base = w.buf.data_ptr()
@@ -362,7 +421,7 @@ def _block_ws(desc, n_nodes, n_edges, which, device, ws):
     need = block_workspace_size(desc, n_nodes, n_edges, which)
     if need == 0:
         raise So2Error(2, "block_workspace_size")
-    return (ws or workspace(device)).get(need)
+    return _default_ws(device, ws).get(need)
 
 
 def _params(w, w_rad, b_rad):
@@ -412,3 +471,245 @@ def block_backward(desc, x, edge_index, edge_vec, w1, w_rad1, b_rad1, w2, w_rad2
                                       *[_ptr(outs[n]) for n in BLOCK_GRADS], p, nb, _stream(dev))
     _check_call(code, "so2conv_block_backward")
     return {n: t for n, t in outs.items() if t is not None}
+
+
+# ---------------------------------------------------------------------------
+# Model operators beside the convolution (include/so2model.h)
+# ---------------------------------------------------------------------------
+NO_PAD = -(1 << 63)
+SCORES = {"softmax": 0, "sigmoid": 1}
+DROP_UNITS = {"element": 0, "channel": 1, "row": 2}
+_TORCH_DTYPE = {SO2_F32: torch.float32, SO2_BF16: torch.bfloat16}
+
+
+def _torch_dtype(code):
+    if code not in _TORCH_DTYPE:
+        raise So2Error(2, "dtype")
+    return _TORCH_DTYPE[code]
+
+
+def _model_ws(need, where, device, ws):
+    """The workspace of one model operator call: the caller's, or a new one
+    from torch's allocator, which belongs to the current stream or to the
+    graph being captured; check() reads the last such call's status."""
+    if need == 0:
+        raise So2Error(2, where)
+    if ws:
+        return ws.get(need)
+    w = Workspace(device)
+    _MODEL_WS[_device(device)] = w
+    return w.get(need)
+
+
+def _need(t, name, shape, dtype, device=None):
+    """`t`, contiguous, after a check of its shape, dtype and device."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, not {t.dtype} of "
+                         f"shape {tuple(t.shape)}")
+    _on_device(t, name, device)
+    return t.contiguous()
+
+
+def _on_device(t, name, device):
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be on {device or 'a CUDA device'}, not {t.device}")
+
+
+def _given_out(out, name, shape, dtype, device):
+    """A caller's output (checked: written in place) or a new one."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if (tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device
+            or not out.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                         f"on {device}")
+    return out
+
+
+def make_embed_desc(n_rows, channels, n_comp=1, scale=1.0, table_dtype=SO2_F32,
+                    out_dtype=SO2_F32, pad_id=None):
+    return EmbedDesc(n_rows, channels, n_comp, float(scale), table_dtype, out_dtype,
+                     NO_PAD if pad_id is None else pad_id)
+
+
+def _rows_of(t, n, inner, name):
+    """Row stride of [n, ...] whose rows are contiguous (`inner` elements)."""
+    want = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size > 1 and stride != want:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        want *= size
+    return inner if n <= 1 else t.stride(0)
+
+
+def embed_forward(desc, ids, table, out=None, ws=None):
+    """so2conv_embed_forward: out [n, n_comp, channels], element rows in
+    component 0.  A given `out` may have any row stride."""
+    lib = load()
+    n = ids.shape[0]
+    ids = _need(ids, "ids", (n,), torch.int64)
+    dev = ids.device
+    table = _need(table, "table", (desc.n_rows, desc.channels), _torch_dtype(desc.table_dtype),
+                  dev)
+    shape, dt = (n, desc.n_comp, desc.channels), _torch_dtype(desc.out_dtype)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=dev)
+    elif tuple(out.shape) != shape or out.dtype != dt or out.device != dev:
+        raise ValueError(f"out must be {dt} of shape {shape} on {dev}")
+    ld = _rows_of(out, n, desc.n_comp * desc.channels, "out")
+    with torch.cuda.device(dev):
+        need = int(lib.so2conv_embed_workspace_size(ctypes.byref(desc), n, WS_FORWARD))
+        p, nb = _model_ws(need, "embed_workspace_size", dev, ws)
+        code = lib.so2conv_embed_forward(ctypes.byref(desc), n, _ptr(ids), _ptr(table),
+                                         out.data_ptr(), ld, p, nb, _stream(dev))
+    _check_call(code, "so2conv_embed_forward")
+    return out
+
+
+def embed_backward(desc, ids, grad_out, out=None, ws=None):
+    """so2conv_embed_backward: grad_table [n_rows, channels] f32.  grad_out is
+    [n, n_comp, channels] (or [n, channels]: its component 0), any row stride."""
+    lib = load()
+    n = ids.shape[0]
+    ids = _need(ids, "ids", (n,), torch.int64)
+    dev = ids.device
+    dt = _torch_dtype(desc.out_dtype)
+    shapes = ((n, desc.n_comp, desc.channels), (n, desc.channels))
+    if tuple(grad_out.shape) not in shapes or grad_out.dtype != dt:
+        raise ValueError(f"grad_out must be {dt} of shape {shapes[0]} or {shapes[1]}")
+    _on_device(grad_out, "grad_out", dev)
+    if grad_out.dim() == 3:
+        grad_out = grad_out[:, 0, :]
+    if desc.channels > 1 and grad_out.stride(1) != 1:
+        grad_out = grad_out.contiguous()
+    if n > 1 and grad_out.stride(0) < desc.channels:  # rows that overlap (an expanded tensor)
+        grad_out = grad_out.contiguous()
+    ld = desc.channels if n <= 1 else grad_out.stride(0)
+    out = _given_out(out, "out", (desc.n_rows, desc.channels), torch.float32, dev)
+    with torch.cuda.device(dev):
+        need = int(lib.so2conv_embed_workspace_size(ctypes.byref(desc), n, WS_BACKWARD))
+        p, nb = _model_ws(need, "embed_workspace_size", dev, ws)
+        code = lib.so2conv_embed_backward(ctypes.byref(desc), n, _ptr(ids), grad_out.data_ptr(),
+                                          ld, _ptr(out), p, nb, _stream(dev))
+    _check_call(code, "so2conv_embed_backward")
+    return out
+
+
+def make_route_desc(n_experts, top_k, score="softmax", n_groups=1, top_groups=1, group_top=1,
+                    renormalise=False, scale=1.0, dtype=SO2_F32):
+    return RouteDesc(n_experts, top_k, n_groups, top_groups, group_top, SCORES[score],
+                     int(bool(renormalise)), float(scale), dtype)
+
+
+def route_forward(desc, logits, bias=None):
+    """so2conv_route_forward: (weights f32, index int32) [n, top_k] and counts
+    int32 [n_experts]."""
+    lib = load()
+    n, dt = logits.shape[0], _torch_dtype(desc.dtype)
+    logits = _need(logits, "logits", (n, desc.n_experts), dt)
+    dev = logits.device
+    if bias is not None:
+        bias = _need(bias, "bias", (desc.n_experts,), torch.float32, dev)
+    weights = torch.empty((n, desc.top_k), dtype=torch.float32, device=dev)
+    index = torch.empty((n, desc.top_k), dtype=torch.int32, device=dev)
+    counts = torch.empty(desc.n_experts, dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        code = lib.so2conv_route_forward(ctypes.byref(desc), n, _ptr(logits), _ptr(bias),
+                                         _ptr(weights), _ptr(index), _ptr(counts), _stream(dev))
+    _check_call(code, "so2conv_route_forward")
+    return weights, index, counts
+
+
+def route_backward(desc, logits, index, grad_weights, out=None):
+    """so2conv_route_backward: grad_logits [n, n_experts] f32."""
+    lib = load()
+    n, dt = logits.shape[0], _torch_dtype(desc.dtype)
+    logits = _need(logits, "logits", (n, desc.n_experts), dt)
+    dev = logits.device
+    index = _need(index, "index", (n, desc.top_k), torch.int32, dev)
+    grad_weights = _need(grad_weights, "grad_weights", (n, desc.top_k), torch.float32, dev)
+    out = _given_out(out, "out", (n, desc.n_experts), torch.float32, dev)
+    with torch.cuda.device(dev):
+        code = lib.so2conv_route_backward(ctypes.byref(desc), n, _ptr(logits), _ptr(index),
+                                          _ptr(grad_weights), _ptr(out), _stream(dev))
+    _check_call(code, "so2conv_route_backward")
+    return out
+
+
+def make_mix_desc(n_experts, n_weights, top_k=None, expert_dtype=SO2_F32, out_dtype=SO2_F32):
+    return MixDesc(n_experts, n_experts if top_k is None else top_k, n_weights, expert_dtype,
+                   out_dtype)
+
+
+def _mix_inputs(desc, experts, weights, index):
+    n = weights.shape[0]
+    experts = _need(experts, "experts", (desc.n_experts, desc.n_weights),
+                    _torch_dtype(desc.expert_dtype))
+    dev = experts.device
+    weights = _need(weights, "weights", (n, desc.top_k), torch.float32, dev)
+    if index is not None:
+        index = _need(index, "index", (n, desc.top_k), torch.int32, dev)
+    return n, dev, experts, weights, index
+
+
+def mix_experts_forward(desc, experts, weights, index=None, out=None, ws=None):
+    """so2conv_mix_experts_forward: out [n_systems, n_weights] of out_dtype."""
+    lib = load()
+    n, dev, experts, weights, index = _mix_inputs(desc, experts, weights, index)
+    out = _given_out(out, "out", (n, desc.n_weights), _torch_dtype(desc.out_dtype), dev)
+    with torch.cuda.device(dev):
+        need = int(lib.so2conv_mix_workspace_size(ctypes.byref(desc), n, WS_FORWARD))
+        p, nb = _model_ws(need, "mix_workspace_size", dev, ws)
+        code = lib.so2conv_mix_experts_forward(ctypes.byref(desc), n, _ptr(experts),
+                                               _ptr(weights), _ptr(index), _ptr(out), p, nb,
+                                               _stream(dev))
+    _check_call(code, "so2conv_mix_experts_forward")
+    return out
+
+
+def mix_experts_backward(desc, experts, weights, grad_out, index=None, need=None, ws=None,
+                         out=None):
+    """so2conv_mix_experts_backward: a dict with grad_experts and grad_weights
+    (those in `need`)."""
+    lib = load()
+    n, dev, experts, weights, index = _mix_inputs(desc, experts, weights, index)
+    grad_out = _need(grad_out, "grad_out", (n, desc.n_weights), torch.float32, dev)
+    names = ["grad_experts", "grad_weights"]
+    need = set(names if need is None else need)
+    shapes = {"grad_experts": (desc.n_experts, desc.n_weights), "grad_weights": (n, desc.top_k)}
+    outs = _outputs(names, need, shapes, out, dict(dtype=torch.float32, device=dev))
+    with torch.cuda.device(dev):
+        size = int(lib.so2conv_mix_workspace_size(ctypes.byref(desc), n, WS_BACKWARD))
+        p, nb = _model_ws(size, "mix_workspace_size", dev, ws)
+        code = lib.so2conv_mix_experts_backward(ctypes.byref(desc), n, _ptr(experts),
+                                                _ptr(weights), _ptr(index), _ptr(grad_out),
+                                                *[_ptr(outs[k]) for k in names], p, nb,
+                                                _stream(dev))
+    _check_call(code, "so2conv_mix_experts_backward")
+    return {k: t for k, t in outs.items() if t is not None}
+
+
+def make_dropout_desc(channels, n_comp=1, unit="channel", p=0.1, dtype=SO2_F32):
+    return DropoutDesc(channels, n_comp, DROP_UNITS[unit], float(p), dtype)
+
+
+def dropout(desc, x, rng, residual=None, rows=None, out=None):
+    """so2conv_dropout: the dropped x [n, n_comp, channels], plus the residual.
+    rng: int64 [2] on the device (key, offset).  The backward is the same call
+    on the gradient, without the residual; `out` may be x or the residual."""
+    lib = load()
+    n, dt = x.shape[0], _torch_dtype(desc.dtype)
+    shape = (n, desc.n_comp, desc.channels)
+    x = _need(x, "x", shape, dt)
+    dev = x.device
+    rng = _need(rng, "rng", (2,), torch.int64, dev)
+    if residual is not None:
+        residual = _need(residual, "residual", shape, dt, dev)
+    if rows is not None:
+        rows = _need(rows, "rows", (n,), torch.int64, dev)
+    out = _given_out(out, "out", shape, dt, dev)
+    with torch.cuda.device(dev):
+        code = lib.so2conv_dropout(ctypes.byref(desc), n, _ptr(x), _ptr(residual), _ptr(rows),
+                                   _ptr(rng), _ptr(out), _stream(dev))
+    _check_call(code, "so2conv_dropout")
+    return out

@@ -1,6 +1,6 @@
 """Build libso2conv.so in-tree with nvcc for sm_100a.
 
-The library is one shared object with a C ABI (include/so2conv.h).  It is
+The library is one shared object with a C ABI (include/so2conv.h and so2model.h).  It is
 linked against the static CUDA runtime and does not link libcuda, so it loads
 (and reports its symbols) on a machine without a GPU.
 
@@ -17,7 +17,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libso2conv.so")
 # translation units, compiled in parallel and linked into one shared object
-SOURCES = ["so2conv_api.cu", "so2conv_dbl_terms.cu"]
+SOURCES = ["so2conv_api.cu", "so2conv_dbl_terms.cu"] + [
+    os.path.join("model", f) for f in ("dropout.cu", "embed.cu", "mix.cu", "route.cu")]
 OBJDIR = os.path.join(HERE, "_build")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -34,9 +35,9 @@ def _nvcc():
 
 
 def _inputs():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)
-             if f.endswith((".cu", ".cuh", ".h"))]
-    files.append(os.path.join(ROOT, "include", "so2conv.h"))
+    files = [os.path.join(d, f) for d in (CSRC, os.path.join(CSRC, "model"))
+             for f in os.listdir(d) if f.endswith((".cu", ".cuh", ".h"))]
+    files += [os.path.join(ROOT, "include", f) for f in ("so2conv.h", "so2model.h")]
     return files
 
 
@@ -53,7 +54,7 @@ def build(force=False, verbose=False, extra=()):
     os.makedirs(OBJDIR, exist_ok=True)
     objs, procs = [], []
     for src in SOURCES:
-        obj = os.path.join(OBJDIR, os.path.splitext(src)[0] + ".o")
+        obj = os.path.join(OBJDIR, os.path.splitext(os.path.basename(src))[0] + ".o")
         cmd = [_nvcc(), *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-c",
                os.path.join(CSRC, src), "-o", obj]
         if verbose:

@@ -1,0 +1,442 @@
+// embed.cu -- element embedding: lookup into the l = 0 rows, and the table's
+// gradient by sorted tokens.
+//
+// Backward.  The tokens are sorted by id (stable, least significant digit
+// first, 8 bits a pass), so that each id's rows are one run of the sorted
+// list.  The list is cut into equal ranges, one warp each; a warp adds its
+// rows in registers and writes every run that lies inside its range straight
+// to the table's gradient.  A run that crosses ranges leaves one partial sum
+// in each, which a second kernel adds in range order.  No atomics on floats:
+// the order of the additions depends on the sizes and the ids alone.
+#include "model_common.cuh"
+
+namespace so2 {
+
+// ---- forward -----------------------------------------------------------------
+template <typename TT, typename TO>
+__global__ void k_embed(int64_t n, const int64_t *__restrict__ ids, const TT *__restrict__ table,
+                        int64_t n_rows, int channels, int64_t row, float scale, int64_t pad_id,
+                        TO *__restrict__ out, int64_t ld_out, DevStatus *st) {
+  const int64_t total = n * row;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t node = i / row, c = i - node * row;
+    float v = 0.f;
+    if (c < channels) {
+      const int64_t id = ids[node];
+      if (id != pad_id) {
+        if (id >= 0 && id < n_rows)
+          v = to_f32(table[id * channels + c]) * scale;
+        else
+          raise_error(st, SO2_ERR_INDEX, (int)(node & 0x7fffffff));
+      }
+    }
+    out[node * ld_out + c] = from_f32<TO>(v);
+  }
+}
+
+// ---- backward: sort ------------------------------------------------------------
+constexpr int SORT_THREADS = 256, SORT_WARPS = 8;
+constexpr int SORT_ROUNDS = 16;                          // 32 keys of a warp each
+constexpr int SORT_TILE = SORT_THREADS * SORT_ROUNDS;    // keys of a block
+constexpr int SORT_BINS = 256;
+
+// The sort key of token i: its id, or n_rows for a token without a gradient.
+__device__ __forceinline__ uint32_t embed_key(const int64_t *ids, int64_t i, int64_t n_rows,
+                                              int64_t pad_id, DevStatus *st) {
+  const int64_t id = ids[i];
+  if (id >= 0 && id < n_rows && id != pad_id) return (uint32_t)id;
+  if (st && id != pad_id) raise_error(st, SO2_ERR_INDEX, (int)(i & 0x7fffffff));
+  return (uint32_t)n_rows;
+}
+
+// hist[bin][block]: keys of the block's tile by digit.  FIRST reads the ids.
+template <bool FIRST>
+__global__ void k_sort_hist(int64_t n, const int64_t *__restrict__ ids, int64_t n_rows,
+                            int64_t pad_id, const uint32_t *__restrict__ keys, int shift,
+                            uint32_t mask, int *__restrict__ hist, DevStatus *st) {
+  __shared__ int h[SORT_BINS];
+  h[threadIdx.x] = 0;
+  __syncthreads();
+  const int64_t t0 = (int64_t)blockIdx.x * SORT_TILE;
+#pragma unroll 4
+  for (int r = 0; r < SORT_ROUNDS; ++r) {
+    const int64_t i = t0 + r * SORT_THREADS + threadIdx.x;
+    if (i < n) {
+      const uint32_t k = FIRST ? embed_key(ids, i, n_rows, pad_id, st) : keys[i];
+      atomicAdd(&h[(k >> shift) & mask], 1);
+    }
+  }
+  __syncthreads();
+  hist[(int64_t)threadIdx.x * gridDim.x + blockIdx.x] = h[threadIdx.x];
+}
+
+// Block-wide exclusive scan of one int per thread (256 threads); *total.
+__device__ __forceinline__ int block_scan256(int v, int *total) {
+  __shared__ int warp_sum[SORT_WARPS];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  if (lane == 31) warp_sum[w] = s;
+  __syncthreads();
+  int base = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < SORT_WARPS; ++i) {
+    if (i < w) base += warp_sum[i];
+    all += warp_sum[i];
+  }
+  __syncthreads();
+  *total = all;
+  return base + s - v;
+}
+
+// One block per bin: its row of hist to exclusive sums over the blocks.
+__global__ void k_sort_scan(int nb, int *__restrict__ hist, int *__restrict__ totals) {
+  int *row = hist + (int64_t)blockIdx.x * nb;
+  int carry = 0;
+  for (int b0 = 0; b0 < nb; b0 += SORT_THREADS) {
+    const int b = b0 + threadIdx.x;
+    const int v = b < nb ? row[b] : 0;
+    int all;
+    const int e = block_scan256(v, &all);
+    if (b < nb) row[b] = carry + e;
+    carry += all;
+  }
+  if (threadIdx.x == 0) totals[blockIdx.x] = carry;
+}
+
+// Stable scatter of the tile: a warp's 512 keys are consecutive, so the order
+// inside the tile is (warp, round, lane).
+template <bool FIRST>
+__global__ void k_sort_scatter(int64_t n, const int64_t *__restrict__ ids, int64_t n_rows,
+                               int64_t pad_id, const uint32_t *__restrict__ keys_in,
+                               const int *__restrict__ perm_in, int shift, uint32_t mask,
+                               const int *__restrict__ hist, const int *__restrict__ totals,
+                               uint32_t *__restrict__ keys_out, int *__restrict__ perm_out) {
+  __shared__ int cnt[SORT_WARPS][SORT_BINS];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+#pragma unroll
+  for (int i = 0; i < SORT_WARPS; ++i) cnt[i][tid] = 0;
+  __syncthreads();
+  const int64_t t0 = (int64_t)blockIdx.x * SORT_TILE + w * (32 * SORT_ROUNDS);
+  uint32_t k[SORT_ROUNDS];
+#pragma unroll
+  for (int r = 0; r < SORT_ROUNDS; ++r) {
+    const int64_t i = t0 + r * 32 + lane;
+    k[r] = 0xffffffffu;
+    if (i < n) {
+      k[r] = FIRST ? embed_key(ids, i, n_rows, pad_id, nullptr) : keys_in[i];
+      atomicAdd(&cnt[w][(k[r] >> shift) & mask], 1);
+    }
+  }
+  int unused;
+  const int first = block_scan256(totals[tid], &unused);  // synchronises the block
+  {
+    int s = first + hist[(int64_t)tid * gridDim.x + blockIdx.x];
+#pragma unroll
+    for (int i = 0; i < SORT_WARPS; ++i) {
+      const int c = cnt[i][tid];
+      cnt[i][tid] = s;
+      s += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < SORT_ROUNDS; ++r) {
+    const int64_t i = t0 + r * 32 + lane;
+    const bool in = i < n;
+    const uint32_t d = in ? (k[r] >> shift) & mask : SORT_BINS;
+    const unsigned same = __match_any_sync(0xffffffffu, d);
+    const int rank = __popc(same & ((1u << lane) - 1));
+    int at = 0;
+    if (in) at = cnt[w][d] + rank;
+    __syncwarp();
+    if (in && rank == 0) cnt[w][d] += __popc(same);
+    __syncwarp();
+    if (in) {
+      keys_out[at] = k[r];
+      perm_out[at] = FIRST ? (int)i : perm_in[i];
+    }
+  }
+}
+
+// ---- backward: sums of the runs --------------------------------------------------
+// One warp per range of `len` sorted tokens and slice of 32 * V channels.
+// head[r]: the range's share of a run that began before it; tail[r]: of a run
+// that begins in it and goes on after it.
+template <int V, typename TG>
+__global__ void k_embed_runs(int64_t n, int64_t n_ranges, int len,
+                             const uint32_t *__restrict__ keys, const int *__restrict__ perm,
+                             uint32_t n_rows, const TG *__restrict__ grad, int64_t ld, int channels,
+                             float scale, float *__restrict__ table, float *__restrict__ head,
+                             float *__restrict__ tail) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int c = (blockIdx.y * 32 + lane) * V;
+  if (r >= n_ranges) return;
+  const int64_t a = r * len, b = a + len < n ? a + len : n;
+  uint32_t cur = keys[a];
+  if (cur >= n_rows) return;
+  const bool on = c < channels;
+  bool from_before = a > 0 && keys[a - 1] == cur;
+  float acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int64_t j = a; j < b; ++j) {
+    const uint32_t k = keys[j];
+    if (k != cur) {
+      if (on) {
+        if (from_before) {
+          store_vec<V>(head + r * channels + c, acc);
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] *= scale;
+          store_vec<V>(table + (int64_t)cur * channels + c, acc);
+        }
+      }
+      from_before = false;
+      cur = k;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = 0.f;
+      if (cur >= n_rows) return;
+    }
+    if (on) {
+      float g[V];
+      load_vec<V>(grad + (int64_t)perm[j] * ld + c, g);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += g[v];
+    }
+  }
+  if (!on) return;
+  const bool goes_on = b < n && keys[b] == cur;
+  if (from_before) {
+    store_vec<V>(head + r * channels + c, acc);
+  } else if (goes_on) {
+    store_vec<V>(tail + r * channels + c, acc);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] *= scale;
+    store_vec<V>(table + (int64_t)cur * channels + c, acc);
+  }
+}
+
+// One block per range: if a run begins in it and goes on after it, its
+// partial sums.  Eight warps take every eighth range of the run.
+template <int V>
+__global__ void k_embed_join(int64_t n, int64_t n_ranges, int len,
+                             const uint32_t *__restrict__ keys, uint32_t n_rows, int channels,
+                             float scale, float *__restrict__ table,
+                             const float *__restrict__ head, const float *__restrict__ tail) {
+  __shared__ float part[8][32 * V];
+  const int64_t r = blockIdx.x;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = (blockIdx.y * 32 + lane) * V;
+  const int64_t a = r * len, b = a + len;
+  if (b >= n) return;
+  const uint32_t key = keys[b - 1];
+  if (key >= n_rows || keys[b] != key || (a > 0 && keys[a - 1] == key)) return;
+  float acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  if (c < channels) {
+    if (w == 0) load_vec<V>(tail + r * channels + c, acc);
+    for (int64_t q = r + 1 + w; q < n_ranges && keys[q * len] == key; q += 8) {
+      float g[V];
+      load_vec<V>(head + q * channels + c, g);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += g[v];
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) part[w][lane * V + v] = acc[v];
+  __syncthreads();
+  if (w == 0 && c < channels) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += part[i][lane * V + v];
+      acc[v] = s * scale;
+    }
+    store_vec<V>(table + (int64_t)key * channels + c, acc);
+  }
+}
+
+}  // namespace so2
+
+using namespace so2;
+
+namespace {
+
+struct EmbedPlan {
+  size_t status, keys[2], perm[2], hist, totals, head, tail, total;
+  int nb, passes, bits, len;
+  int64_t n_ranges;
+};
+
+bool embed_ok(const so2conv_embed_desc *d) {
+  return d->n_rows >= 1 && d->n_rows < 0x7fffffff && d->channels >= 1 && d->channels <= 65536 &&
+         d->n_comp >= 1 && d->n_comp <= 1024 && dtype_ok(d->table_dtype) && dtype_ok(d->out_dtype);
+}
+
+EmbedPlan embed_plan(const so2conv_embed_desc *d, int64_t n, int which) {
+  EmbedPlan p{};
+  size_t c = 0;
+  p.status = ws_take(c, sizeof(DevStatus));
+  if (which == SO2_WS_BACKWARD && n > 0) {
+    int bits = 1;  // of the keys 0..n_rows
+    while ((d->n_rows >> bits) != 0) ++bits;
+    p.passes = (bits + 7) / 8;
+    p.bits = (bits + p.passes - 1) / p.passes;
+    p.nb = (int)ceil_div(n, SORT_TILE);
+    // about 32 warps of ranges for each SM, of 8 tokens at least
+    const int64_t len = ceil_div(n, MODEL_SMS * 32);
+    p.len = (int)(len < 8 ? 8 : len);
+    p.n_ranges = ceil_div(n, p.len);
+    for (int i = 0; i < 2; ++i) {
+      p.keys[i] = ws_take(c, sizeof(uint32_t) * n);
+      p.perm[i] = ws_take(c, sizeof(int) * n);
+    }
+    p.hist = ws_take(c, sizeof(int) * SORT_BINS * (size_t)p.nb);
+    p.totals = ws_take(c, sizeof(int) * SORT_BINS);
+    p.head = ws_take(c, sizeof(float) * p.n_ranges * d->channels);
+    p.tail = ws_take(c, sizeof(float) * p.n_ranges * d->channels);
+  }
+  p.total = (c + 255) & ~static_cast<size_t>(255);
+  return p;
+}
+
+so2_status embed_checks(const so2conv_embed_desc *d, int64_t n, const int64_t *ids, void *ws,
+                        size_t ws_bytes, int which, EmbedPlan &p) {
+  if (!d) return SO2_ERR_INVALID_ARG;
+  if (!embed_ok(d)) return SO2_ERR_UNSUPPORTED;
+  if (n < 0 || n > (1ll << 30) || (n > 0 && !ids) || !aligned_to(ids, 8)) return SO2_ERR_INVALID_ARG;
+  if (!ws || !aligned_to(ws, 256)) return SO2_ERR_WORKSPACE;
+  p = embed_plan(d, n, which);
+  if (ws_bytes < p.total) return SO2_ERR_WORKSPACE;
+  return SO2_OK;
+}
+
+template <typename TT, typename TO>
+void launch_embed(const so2conv_embed_desc *d, int64_t n, const int64_t *ids, const void *table,
+                  void *out, int64_t ld, DevStatus *st, cudaStream_t s) {
+  const int64_t row = (int64_t)d->n_comp * d->channels;
+  const int64_t want = ceil_div(n * row, 256);
+  const int grid = (int)(want < MODEL_SMS * 16 ? want : MODEL_SMS * 16);
+  k_embed<TT, TO><<<grid, 256, 0, s>>>(n, ids, static_cast<const TT *>(table), d->n_rows,
+                                       d->channels, row, d->scale, d->pad_id,
+                                       static_cast<TO *>(out), ld, st);
+}
+
+template <int V, typename TG>
+so2_status embed_sums(const so2conv_embed_desc *d, int64_t n, const EmbedPlan &p, void *ws,
+                      const uint32_t *keys, const int *perm, const void *grad, int64_t ld,
+                      float *table, cudaStream_t s) {
+  const int slices = (int)ceil_div(d->channels, 32 * V);
+  float *head = ws_at<float>(ws, p.head), *tail = ws_at<float>(ws, p.tail);
+  k_embed_runs<V, TG><<<dim3((unsigned)ceil_div(p.n_ranges, 8), slices), 256, 0, s>>>(
+      n, p.n_ranges, p.len, keys, perm, (uint32_t)d->n_rows, static_cast<const TG *>(grad), ld,
+      d->channels, d->scale, table, head, tail);
+  MODEL_CKL();
+  if (p.n_ranges > 1) {
+    k_embed_join<V><<<dim3((unsigned)p.n_ranges, slices), 256, 0, s>>>(
+        n, p.n_ranges, p.len, keys, (uint32_t)d->n_rows, d->channels, d->scale, table, head, tail);
+    MODEL_CKL();
+  }
+  return SO2_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t so2conv_embed_workspace_size(const so2conv_embed_desc *desc, int64_t n, int which) {
+  if (!desc || !embed_ok(desc) || n < 0 || n > (1ll << 30) ||
+      (which != SO2_WS_FORWARD && which != SO2_WS_BACKWARD))
+    return 0;
+  return embed_plan(desc, n, which).total;
+}
+
+so2_status so2conv_embed_forward(const so2conv_embed_desc *d, int64_t n, const int64_t *ids,
+                                 const void *table, void *out, int64_t ld_out, void *ws,
+                                 size_t ws_bytes, so2_stream_t stream) {
+  EmbedPlan p;
+  so2_status r = embed_checks(d, n, ids, ws, ws_bytes, SO2_WS_FORWARD, p);
+  if (r != SO2_OK) return r;
+  if (ld_out < (int64_t)d->n_comp * d->channels || ld_out > (1ll << 40)) return SO2_ERR_INVALID_ARG;
+  if (n > 0 && (!table || !out || !aligned_to(table, dtype_size(d->table_dtype)) ||
+                !aligned_to(out, dtype_size(d->out_dtype))))
+    return SO2_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DevStatus *st = ws_at<DevStatus>(ws, p.status);
+  MODEL_CK(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
+  if (n == 0) return SO2_OK;
+  typedef __nv_bfloat16 bf;
+  if (d->table_dtype == SO2_F32 && d->out_dtype == SO2_F32)
+    launch_embed<float, float>(d, n, ids, table, out, ld_out, st, s);
+  else if (d->table_dtype == SO2_F32)
+    launch_embed<float, bf>(d, n, ids, table, out, ld_out, st, s);
+  else if (d->out_dtype == SO2_F32)
+    launch_embed<bf, float>(d, n, ids, table, out, ld_out, st, s);
+  else
+    launch_embed<bf, bf>(d, n, ids, table, out, ld_out, st, s);
+  MODEL_CKL();
+  return SO2_OK;
+}
+
+so2_status so2conv_embed_backward(const so2conv_embed_desc *d, int64_t n, const int64_t *ids,
+                                  const void *grad_out, int64_t ld_grad, float *grad_table,
+                                  void *ws, size_t ws_bytes, so2_stream_t stream) {
+  EmbedPlan p;
+  so2_status r = embed_checks(d, n, ids, ws, ws_bytes, SO2_WS_BACKWARD, p);
+  if (r != SO2_OK) return r;
+  if (!grad_table || !aligned_to(grad_table, 4) || ld_grad < d->channels || ld_grad > (1ll << 40))
+    return SO2_ERR_INVALID_ARG;
+  const size_t es = dtype_size(d->out_dtype);
+  if (n > 0 && (!grad_out || !aligned_to(grad_out, es))) return SO2_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DevStatus *st = ws_at<DevStatus>(ws, p.status);
+  MODEL_CK(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
+  MODEL_CK(cudaMemsetAsync(grad_table, 0, sizeof(float) * d->n_rows * d->channels, s));
+  if (n == 0) return SO2_OK;
+  int *hist = ws_at<int>(ws, p.hist), *totals = ws_at<int>(ws, p.totals);
+  const uint32_t mask = (1u << p.bits) - 1;
+  for (int q = 0; q < p.passes; ++q) {
+    const uint32_t *ki = ws_at<uint32_t>(ws, p.keys[(q + 1) & 1]);
+    const int *pi = ws_at<int>(ws, p.perm[(q + 1) & 1]);
+    uint32_t *ko = ws_at<uint32_t>(ws, p.keys[q & 1]);
+    int *po = ws_at<int>(ws, p.perm[q & 1]);
+    const int shift = q * p.bits;
+    if (q == 0)
+      k_sort_hist<true><<<p.nb, SORT_THREADS, 0, s>>>(n, ids, d->n_rows, d->pad_id, nullptr, shift,
+                                                      mask, hist, st);
+    else
+      k_sort_hist<false><<<p.nb, SORT_THREADS, 0, s>>>(n, nullptr, 0, 0, ki, shift, mask, hist, st);
+    MODEL_CKL();
+    k_sort_scan<<<SORT_BINS, SORT_THREADS, 0, s>>>(p.nb, hist, totals);
+    MODEL_CKL();
+    if (q == 0)
+      k_sort_scatter<true><<<p.nb, SORT_THREADS, 0, s>>>(n, ids, d->n_rows, d->pad_id, nullptr,
+                                                         nullptr, shift, mask, hist, totals, ko, po);
+    else
+      k_sort_scatter<false><<<p.nb, SORT_THREADS, 0, s>>>(n, nullptr, 0, 0, ki, pi, shift, mask,
+                                                          hist, totals, ko, po);
+    MODEL_CKL();
+  }
+  const uint32_t *keys = ws_at<uint32_t>(ws, p.keys[(p.passes + 1) & 1]);
+  const int *perm = ws_at<int>(ws, p.perm[(p.passes + 1) & 1]);
+  // rows in vectors of four where every row starts on one's boundary
+  const bool vec = d->channels % 4 == 0 && ld_grad % 4 == 0 && aligned_to(grad_out, 4 * es) &&
+                   aligned_to(grad_table, 16);
+  if (d->out_dtype == SO2_F32)
+    return vec ? embed_sums<4, float>(d, n, p, ws, keys, perm, grad_out, ld_grad, grad_table, s)
+               : embed_sums<1, float>(d, n, p, ws, keys, perm, grad_out, ld_grad, grad_table, s);
+  return vec ? embed_sums<4, __nv_bfloat16>(d, n, p, ws, keys, perm, grad_out, ld_grad, grad_table, s)
+             : embed_sums<1, __nv_bfloat16>(d, n, p, ws, keys, perm, grad_out, ld_grad, grad_table, s);
+}
+
+}  // extern "C"

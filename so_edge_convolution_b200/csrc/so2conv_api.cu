@@ -13,6 +13,10 @@
 #include "edge_kernels.cuh"
 #include "gemm_tc.cuh"
 
+namespace so2 {
+extern long long g_model_launches;  // the model operators' own count (model/)
+}
+
 using namespace so2;
 
 #ifndef SO2_SCATTER_PAIR_STAGES  // pipeline stages of the CTA-pair product with the fused epilogue
@@ -1630,7 +1634,7 @@ so2_status so2conv_check(void *ws, so2_stream_t stream) {
   return static_cast<so2_status>(h.code);
 }
 
-long long so2conv_launch_count(void) { return g_launches; }
+long long so2conv_launch_count(void) { return g_launches + g_model_launches; }
 
 so2_status so2conv_wait_selftest(void *ws, size_t ws_bytes, int64_t limit_us,
                                  so2_stream_t stream) {
@@ -1682,7 +1686,7 @@ const char *so2conv_status_string(so2_status s) {
     case SO2_ERR_UNSUPPORTED: return "unsupported shape or option";
     case SO2_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case SO2_ERR_CUDA: return "CUDA runtime error";
-    case SO2_ERR_INDEX: return "edge index outside [0, n_nodes)";
+    case SO2_ERR_INDEX: return "an index outside its range";
     case SO2_ERR_TIMEOUT: return "a bounded device wait gave up";
     case SO2_ERR_DEGENERATE: return "zero-length edge vector";
   }
