@@ -7,7 +7,115 @@
 
 namespace so2 {
 
-// ---- forward -----------------------------------------------------------------
+// ---- every expert in order: rows of a skinny product -------------------------------
+// C[r, :] = sum_s M[r, s] B[s, :], with M[r * mr + s * ms] in f32: the forward
+// (r = t, s = e, B = experts) and the experts' gradient (r = e, s = t, B =
+// grad_out).  A thread owns V columns and TT rows of C in registers and reads
+// each row of B once for them, through a ring of asynchronous copies that
+// only it reads (no block barrier in the loop).  Two rows of C share one
+// packed FMA; the weights lie in shared memory, pairs of rows side by side.
+constexpr int ROWS_THREADS = 128;
+constexpr int ROWS_SC = 32;     // rows of B whose weights are staged together
+constexpr int ROWS_DEPTH = 8;   // copies in flight
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void fma2(uint64_t &d, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *dst, const void *src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int TT, int V, typename TB, typename TC>
+__global__ void __launch_bounds__(ROWS_THREADS)
+    k_mix_rows(int R, int S, int64_t n, const float *__restrict__ M, int64_t mr, int64_t ms,
+               const TB *__restrict__ Bm, TC *__restrict__ C) {
+  constexpr int PAIRS = (TT + 1) / 2;
+  constexpr bool RING = V > 1;
+  constexpr int BYTES = V * (int)sizeof(TB);
+  __shared__ __align__(16) float wts[ROWS_SC][2 * PAIRS];
+  __shared__ __align__(16) unsigned char ring[RING ? ROWS_DEPTH : 1][ROWS_THREADS][RING ? BYTES : 4];
+  const int tid = threadIdx.x;
+  const int64_t c = (blockIdx.x * (int64_t)ROWS_THREADS + tid) * V;
+  const bool on = c < n;
+  const TB *col = Bm + c;
+  for (int r0 = 0; r0 < R; r0 += TT) {
+    uint64_t acc[PAIRS][V];
+#pragma unroll
+    for (int p = 0; p < PAIRS; ++p)
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[p][v] = 0;
+    if constexpr (RING) {
+#pragma unroll
+      for (int d = 0; d < ROWS_DEPTH - 1; ++d) {
+        if (on && d < S) copy_async<BYTES>(ring[d][tid], col + d * n);
+        copy_commit();
+      }
+    }
+    for (int s0 = 0; s0 < S; s0 += ROWS_SC) {
+      __syncthreads();
+      for (int i = tid; i < ROWS_SC * 2 * PAIRS; i += ROWS_THREADS) {
+        const int s = s0 + i / (2 * PAIRS), r = r0 + i % (2 * PAIRS);
+        wts[i / (2 * PAIRS)][i % (2 * PAIRS)] =
+            (s < S && r < R && i % (2 * PAIRS) < TT) ? M[r * mr + s * ms] : 0.f;
+      }
+      __syncthreads();
+      const int end = S - s0 < ROWS_SC ? S - s0 : ROWS_SC;
+#pragma unroll 4
+      for (int i = 0; i < end; ++i) {
+        const int s = s0 + i;
+        float x[V];
+        if constexpr (RING) {
+          const int nx = s + ROWS_DEPTH - 1;
+          if (on && nx < S) copy_async<BYTES>(ring[nx % ROWS_DEPTH][tid], col + nx * n);
+          copy_commit();
+          copy_wait<ROWS_DEPTH - 1>();
+          load_vec<V>(reinterpret_cast<const TB *>(ring[s % ROWS_DEPTH][tid]), x);
+        } else {
+          x[0] = on ? to_f32(col[s * n]) : 0.f;
+        }
+        uint64_t xx[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) xx[v] = pack2(x[v], x[v]);
+#pragma unroll
+        for (int p = 0; p < PAIRS; ++p) {
+          const uint64_t w = *reinterpret_cast<const uint64_t *>(&wts[i][2 * p]);
+#pragma unroll
+          for (int v = 0; v < V; ++v) fma2(acc[p][v], w, xx[v]);
+        }
+      }
+    }
+    if (on) {
+#pragma unroll
+      for (int q = 0; q < TT; ++q) {
+        if (r0 + q < R) {
+          float o[V];
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            o[v] = __uint_as_float((uint32_t)(acc[q >> 1][v] >> (32 * (q & 1))));
+          store_vec<V>(C + (int64_t)(r0 + q) * n + c, o);
+        }
+      }
+    }
+    if constexpr (RING) copy_wait<0>();
+  }
+}
+
+// ---- forward, by index -------------------------------------------------------------
 template <int V, typename TE, typename TO>
 __global__ void k_mix(int64_t n_systems, int K, int top_k, int64_t n, const TE *__restrict__ experts,
                       const float *__restrict__ weights, const int *__restrict__ index,
@@ -20,7 +128,7 @@ __global__ void k_mix(int64_t n_systems, int K, int top_k, int64_t n, const TE *
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
     for (int j = 0; j < top_k; ++j) {
       const int64_t p = t * top_k + j;
-      const int e = index ? index[p] : j;
+      const int e = index[p];
       if (e < 0 || e >= K) {
         if (e != -1 && c == 0) raise_error(st, SO2_ERR_INDEX, (int)p);
         continue;
@@ -36,28 +144,31 @@ __global__ void k_mix(int64_t n_systems, int K, int top_k, int64_t n, const TE *
 }
 
 // ---- backward ------------------------------------------------------------------
-// Lists of the slots by expert: offsets [K+1], slots in slot order.
+// Lists of the slots by expert: offsets [K+1], slots in slot order.  One warp
+// per expert: the slots of lower experts give its offset, its own follow.
 __global__ void k_mix_lists(int n_slots, int K, const int *__restrict__ index,
                             int *__restrict__ offsets, int *__restrict__ list, DevStatus *st) {
-  for (int p = threadIdx.x; p < n_slots; p += blockDim.x) {
-    const int e = index[p];
-    if (e < -1 || e >= K) raise_error(st, SO2_ERR_INDEX, p);
+  const int lane = threadIdx.x & 31;
+  const int e = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (e >= K) return;
+  int lower = 0, mine = 0;
+  for (int p0 = 0; p0 < n_slots; p0 += 32) {
+    const int p = p0 + lane, v = p < n_slots ? index[p] : -1;
+    lower += __popc(__ballot_sync(0xffffffffu, v >= 0 && v < e));
+    mine += __popc(__ballot_sync(0xffffffffu, v == e));
+    if (e == 0 && (v < -1 || v >= K)) raise_error(st, SO2_ERR_INDEX, p);
   }
-  for (int e = threadIdx.x; e < K; e += blockDim.x) {
-    int c = 0;
-    for (int p = 0; p < n_slots; ++p) c += index[p] == e;
-    offsets[e + 1] = c;
+  if (lane == 0) {
+    offsets[e] = lower;
+    if (e == K - 1) offsets[K] = lower + mine;
   }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    offsets[0] = 0;
-    for (int e = 0; e < K; ++e) offsets[e + 1] += offsets[e];
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < K; e += blockDim.x) {
-    int at = offsets[e];
-    for (int p = 0; p < n_slots; ++p)
-      if (index[p] == e) list[at++] = p;
+  if (mine == 0) return;
+  int at = lower;
+  for (int p0 = 0; p0 < n_slots; p0 += 32) {
+    const int p = p0 + lane;
+    const unsigned m = __ballot_sync(0xffffffffu, p < n_slots && index[p] == e);
+    if ((m >> lane) & 1) list[at + __popc(m & ((1u << lane) - 1))] = p;
+    at += __popc(m);
   }
 }
 
@@ -69,12 +180,12 @@ __global__ void k_mix_grad_experts(int64_t n_systems, int K, int top_k, int64_t 
   const int64_t c = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) * V;
   if (c >= n) return;
   for (int e = blockIdx.y; e < K; e += gridDim.y) {
-    const int a = offsets ? offsets[e] : 0, b = offsets ? offsets[e + 1] : (int)n_systems;
+    const int a = offsets[e], b = offsets[e + 1];
     float acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
     for (int q = a; q < b; ++q) {
-      const int p = offsets ? list[q] : q * top_k + e;
+      const int p = list[q];
       const float w = weights[p];
       float g[V];
       load_vec<V>(grad + (int64_t)(p / top_k) * n + c, g);
@@ -85,47 +196,176 @@ __global__ void k_mix_grad_experts(int64_t n_systems, int K, int top_k, int64_t 
   }
 }
 
-constexpr int DOT_SPLITS = 16;
+// ---- the routing weights' gradient: products over all columns --------------------------
+// Every (t, e) of a tile of 64 systems and 32 experts, over the block's share
+// of the columns.  Tiles of both operands go through shared memory in three
+// stages of asynchronous copies; a thread holds 8 x 4 products, two columns to
+// a packed FMA (their halves are added at the end), and reads 12 vectors of
+// four columns for 64 of them.  Four groups of 64 threads take every fourth
+// vector.  Row pitches are 4 words off a multiple of 32, so the eight rows of
+// a warp's read lie in different banks.
+constexpr int DOT_T = 64, DOT_E = 32, DOT_COLS = 64, DOT_STAGES = 3;
+constexpr int DOT_PITCH_G = DOT_COLS + 4;  // f32 elements
+template <typename TE> constexpr int dot_pitch_e() { return DOT_COLS + 16 / (int)sizeof(TE); }
+template <typename TE> constexpr int dot_stage_bytes() {
+  return DOT_T * DOT_PITCH_G * 4 + DOT_E * dot_pitch_e<TE>() * (int)sizeof(TE);
+}
 
+template <int BYTES>
+__device__ __forceinline__ void copy_async_or_zero(void *dst, const void *src, bool on) {
+  const int have = on ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(have)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src),
+                 "n"(BYTES), "r"(have)
+                 : "memory");
+}
+
+// One stage: rows [row0, rows) and columns [c0, n) of a matrix, zero outside.
+template <int ROWS, int PITCH, bool VEC, typename T>
+__device__ __forceinline__ void dot_load(T *dst, const T *src, int row0, int rows, int64_t c0, int64_t n) {
+  constexpr int V = VEC ? 4 : 1, PER_ROW = DOT_COLS / V;
+  for (int i = threadIdx.x; i < ROWS * PER_ROW; i += 256) {
+    const int r = i / PER_ROW, c = (i % PER_ROW) * V;
+    const bool on = row0 + r < rows && c0 + c < n;
+    const T *from = on ? src + (int64_t)(row0 + r) * n + c0 + c : src;
+    if constexpr (VEC)
+      copy_async_or_zero<V * (int)sizeof(T)>(dst + r * PITCH + c, from, on);
+    else
+      dst[r * PITCH + c] = on ? *from : from_f32<T>(0.f);
+  }
+}
+
+// part[split][t][e], with blockIdx.x the split, blockIdx.y the tile.
+template <bool VEC, typename TE>
+__global__ void __launch_bounds__(256, 2)
+    k_mix_dot_tiles(int T, int K, int64_t n, const TE *__restrict__ experts,
+                    const float *__restrict__ grad, float *__restrict__ part) {
+  extern __shared__ __align__(16) unsigned char sm[];
+  constexpr int PE = dot_pitch_e<TE>(), STAGE = dot_stage_bytes<TE>();
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int tg = lane & 7, eg = (lane >> 3) + 4 * (w & 1), cg = w >> 1;
+  const int etiles = (K + DOT_E - 1) / DOT_E;
+  const int t0 = (blockIdx.y / etiles) * DOT_T, e0 = (blockIdx.y % etiles) * DOT_E;
+  const int64_t tiles = (n + DOT_COLS - 1) / DOT_COLS;
+  const int64_t first = tiles * blockIdx.x / gridDim.x, last = tiles * (blockIdx.x + 1) / gridDim.x;
+  auto g_of = [&](int64_t i) { return reinterpret_cast<float *>(sm + (i % DOT_STAGES) * STAGE); };
+  auto e_of = [&](int64_t i) {
+    return reinterpret_cast<TE *>(sm + (i % DOT_STAGES) * STAGE + DOT_T * DOT_PITCH_G * 4);
+  };
+  auto load = [&](int64_t i) {
+    if (i < last) {
+      dot_load<DOT_T, DOT_PITCH_G, VEC>(g_of(i), grad, t0, T, i * DOT_COLS, n);
+      dot_load<DOT_E, PE, VEC>(e_of(i), experts, e0, K, i * DOT_COLS, n);
+    }
+    copy_commit();
+  };
+  uint64_t acc[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0;
+#pragma unroll
+  for (int i = 0; i < DOT_STAGES - 1; ++i) load(first + i);
+  for (int64_t i = first; i < last; ++i) {
+    copy_wait<DOT_STAGES - 2>();
+    __syncthreads();  // stage i is there, and everyone is done with stage i - 1
+    load(i + DOT_STAGES - 1);
+    const float *g = g_of(i);
+    const TE *x = e_of(i);
+#pragma unroll
+    for (int q = cg; q < DOT_COLS / 4; q += 4) {
+      uint64_t gv[8][2], xv[4][2];
+#pragma unroll
+      for (int a = 0; a < 8; ++a) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(g + (tg + 8 * a) * DOT_PITCH_G + 4 * q);
+        gv[a][0] = v.x, gv[a][1] = v.y;
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        float f[4];
+        load_vec<4>(x + (eg + 8 * b) * PE + 4 * q, f);
+        xv[b][0] = pack2(f[0], f[1]), xv[b][1] = pack2(f[2], f[3]);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int a = 0; a < 8; ++a)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) fma2(acc[a][b], gv[a][h], xv[b][h]);
+    }
+  }
+  copy_wait<0>();
+  __syncthreads();
+  // the four column groups' sums, in order
+  float *red = reinterpret_cast<float *>(sm);  // [4][DOT_T][DOT_E]
+#pragma unroll
+  for (int a = 0; a < 8; ++a)
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      red[(cg * DOT_T + tg + 8 * a) * DOT_E + eg + 8 * b] =
+          __uint_as_float((uint32_t)acc[a][b]) + __uint_as_float((uint32_t)(acc[a][b] >> 32));
+  __syncthreads();
+  for (int i = tid; i < DOT_T * DOT_E; i += 256) {
+    const int t = t0 + i / DOT_E, e = e0 + i % DOT_E;
+    if (t < T && e < K)
+      part[(int64_t)blockIdx.x * T * K + (int64_t)t * K + e] =
+          (red[i] + red[DOT_T * DOT_E + i]) + (red[2 * DOT_T * DOT_E + i] + red[3 * DOT_T * DOT_E + i]);
+  }
+}
+
+// One slot a warp over the block's share of the columns: part[split][slot].
 template <int V, typename TE>
-__global__ void k_mix_dots(int64_t n_slots, int K, int top_k, int64_t n,
-                           const TE *__restrict__ experts, const int *__restrict__ index,
-                           const float *__restrict__ grad, float *__restrict__ part) {
-  __shared__ float ws[8];
-  for (int64_t p = blockIdx.y; p < n_slots; p += gridDim.y) {
-    const int e = index ? index[p] : (int)(p % top_k);
-    float s = 0.f;
+__global__ void k_mix_dot_slots(int64_t n_slots, int K, int top_k, int64_t n,
+                                const TE *__restrict__ experts, const int *__restrict__ index,
+                                const float *__restrict__ grad, float *__restrict__ part) {
+  const int lane = threadIdx.x & 31;
+  const int64_t len = ((n + gridDim.x - 1) / gridDim.x + V - 1) / V * V;
+  const int64_t c0 = blockIdx.x * len, c1 = c0 + len < n ? c0 + len : n;
+  for (int64_t p = blockIdx.y * 8 + (threadIdx.x >> 5); p < n_slots; p += gridDim.y * 8) {
+    const int e = index[p];
+    float s[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = 0.f;
     if (e >= 0 && e < K) {
       const TE *x = experts + e * n;
       const float *g = grad + (p / top_k) * n;
-      for (int64_t c = (blockIdx.x * 256ll + threadIdx.x) * V; c < n; c += DOT_SPLITS * 256ll * V) {
+#pragma unroll 4
+      for (int64_t c = c0 + lane * V; c < c1; c += 32 * V) {
         float a[V], b[V];
         load_vec<V>(x + c, a);
         load_vec<V>(g + c, b);
 #pragma unroll
-        for (int v = 0; v < V; ++v) s = fmaf(a[v], b[v], s);
+        for (int v = 0; v < V; ++v) s[v] = fmaf(a[v], b[v], s[v]);
       }
     }
+    float sum = s[0];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if ((threadIdx.x & 31) == 0) ws[threadIdx.x >> 5] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      s = 0.f;
-      for (int i = 0; i < 8; ++i) s += ws[i];
-      part[blockIdx.x * n_slots + p] = s;
-    }
-    __syncthreads();
+    for (int v = 1; v < V; ++v) sum += s[v];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) part[blockIdx.x * n_slots + p] = sum;
   }
 }
 
-__global__ void k_mix_dots_join(int64_t n_slots, int splits, const float *__restrict__ part,
-                                float *__restrict__ gw) {
-  const int64_t p = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+// gw[slot] from the splits: of all (t, e) (all) or of the slots.  One warp a slot.
+__global__ void k_mix_dots_join(int64_t n_slots, int K, int top_k, const int *__restrict__ index,
+                                bool all, int64_t stride, int splits,
+                                const float *__restrict__ part, float *__restrict__ gw) {
+  const int lane = threadIdx.x & 31;
+  const int64_t p = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5);
   if (p >= n_slots) return;
+  const int e = index ? index[p] : (int)(p % top_k);
   float s = 0.f;
-  for (int i = 0; i < splits; ++i) s += part[i * n_slots + p];
-  gw[p] = s;
+  if (e >= 0 && e < K) {
+    const int64_t at = all ? (p / top_k) * K + e : p;
+    for (int i = lane; i < splits; i += 32) s += part[i * stride + at];
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) gw[p] = s;
 }
 
 }  // namespace so2
@@ -136,6 +376,8 @@ namespace {
 
 struct MixPlan {
   size_t status, offsets, list, part, total;
+  bool tiles;  // the products of all (t, e), or of the slots alone
+  int splits;
 };
 
 bool mix_ok(const so2conv_mix_desc *d) {
@@ -156,7 +398,23 @@ MixPlan mix_plan(const so2conv_mix_desc *d, int64_t n_systems, int which) {
     const size_t slots = (size_t)(n_systems * d->top_k);
     p.offsets = ws_take(c, sizeof(int) * (d->n_experts + 1));
     p.list = ws_take(c, sizeof(int) * slots);
-    p.part = ws_take(c, sizeof(float) * slots * DOT_SPLITS);
+    // A product costs a tile about an eighth of what it costs by slot (12
+    // vector reads for 256 products against 2 for 4), so tiles where the slots
+    // name that share of the experts.
+    p.tiles = d->top_k * 8 >= d->n_experts;
+    const int64_t per = p.tiles ? n_systems * d->n_experts : n_systems * d->top_k;  // products
+    int64_t want;
+    if (p.tiles) {  // two resident blocks an SM
+      const int64_t t = ceil_div(n_systems, DOT_T) * ceil_div(d->n_experts, DOT_E);
+      want = ceil_div(2 * MODEL_SMS, t > 0 ? t : 1);
+      if (want > ceil_div(d->n_weights, DOT_COLS)) want = ceil_div(d->n_weights, DOT_COLS);
+    } else {
+      want = ceil_div(d->n_weights, 2048);
+    }
+    // at most 16 M partial sums
+    const int64_t most = per > 0 ? (16ll << 20) / per : 1;
+    p.splits = (int)(want < most ? want : (most > 0 ? most : 1));
+    p.part = ws_take(c, sizeof(float) * (size_t)(per * p.splits));
   }
   p.total = (c + 255) & ~static_cast<size_t>(255);
   return p;
@@ -179,10 +437,34 @@ so2_status mix_checks(const so2conv_mix_desc *d, int64_t n_systems, const void *
   return SO2_OK;
 }
 
+// Rows of C a thread holds: all of them up to 32, else the fewest passes over B
+// with evenly filled ones.
+template <int V, typename TB, typename TC>
+void launch_rows(int R, int S, int64_t n, const float *M, int64_t mr, int64_t ms, const TB *B, TC *C,
+                 cudaStream_t s) {
+  const unsigned grid = (unsigned)ceil_div(n, ROWS_THREADS * V);
+  const int passes = (R + 31) / 32, tt = (R + passes - 1) / passes;
+#define MIX_ROWS(TT) \
+  k_mix_rows<TT, V, TB, TC><<<grid, ROWS_THREADS, 0, s>>>(R, S, n, M, mr, ms, B, C)
+  if (tt <= 1) MIX_ROWS(1);
+  else if (tt <= 2) MIX_ROWS(2);
+  else if (tt <= 4) MIX_ROWS(4);
+  else if (tt <= 8) MIX_ROWS(8);
+  else if (tt <= 16) MIX_ROWS(16);
+  else if (tt <= 24) MIX_ROWS(24);
+  else MIX_ROWS(32);
+#undef MIX_ROWS
+}
+
 template <int V, typename TE, typename TO>
 void launch_mix(const so2conv_mix_desc *d, int64_t n_systems, const void *experts,
                 const float *weights, const int32_t *index, void *out, DevStatus *st,
                 cudaStream_t s) {
+  if (!index) {
+    launch_rows<V>((int)n_systems, d->n_experts, d->n_weights, weights, d->top_k, 1,
+                   static_cast<const TE *>(experts), static_cast<TO *>(out), s);
+    return;
+  }
   const dim3 grid((unsigned)ceil_div(d->n_weights, 256 * V), (unsigned)(n_systems < 4 ? n_systems : 4));
   k_mix<V, TE, TO><<<grid, 256, 0, s>>>(n_systems, d->n_experts, d->top_k, d->n_weights,
                                         static_cast<const TE *>(experts), weights, index,
@@ -197,6 +479,29 @@ void launch_mix(bool vec, const so2conv_mix_desc *d, int64_t n_systems, const vo
     launch_mix<4, TE, TO>(d, n_systems, experts, weights, index, out, st, s);
   else
     launch_mix<1, TE, TO>(d, n_systems, experts, weights, index, out, st, s);
+}
+
+template <bool VEC, typename TE>
+so2_status mix_dots(const so2conv_mix_desc *d, int64_t n_systems, const MixPlan &p,
+                    const void *experts, const int32_t *index, const float *grad, float *part,
+                    cudaStream_t s) {
+  const TE *x = static_cast<const TE *>(experts);
+  const int64_t slots = n_systems * d->top_k;
+  if (p.tiles) {
+    constexpr int red = 4 * DOT_T * DOT_E * 4;
+    constexpr int smem = DOT_STAGES * dot_stage_bytes<TE>() > red ? DOT_STAGES * dot_stage_bytes<TE>() : red;
+    MODEL_CK(cudaFuncSetAttribute(k_mix_dot_tiles<VEC, TE>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    const int64_t tiles = ceil_div(n_systems, DOT_T) * ceil_div(d->n_experts, DOT_E);
+    k_mix_dot_tiles<VEC, TE><<<dim3(p.splits, (unsigned)tiles), 256, smem, s>>>(
+        (int)n_systems, d->n_experts, d->n_weights, x, grad, part);
+  } else {
+    const int64_t rows = ceil_div(slots, 8);
+    k_mix_dot_slots<VEC ? 4 : 1, TE><<<dim3(p.splits, (unsigned)(rows < 16 ? rows : 16)), 256, 0, s>>>(
+        slots, d->n_experts, d->top_k, d->n_weights, x, index, grad, part);
+  }
+  MODEL_CKL();
+  return SO2_OK;
 }
 
 }  // namespace
@@ -262,7 +567,7 @@ so2_status so2conv_mix_experts_backward(const so2conv_mix_desc *d, int64_t n_sys
   if (index) {
     offsets = ws_at<int>(ws, p.offsets);
     list = ws_at<int>(ws, p.list);
-    k_mix_lists<<<1, 1024, 0, s>>>((int)slots, K, index, offsets, list, st);
+    k_mix_lists<<<(unsigned)ceil_div(K, 8), 256, 0, s>>>((int)slots, K, index, offsets, list, st);
     MODEL_CKL();
   }
   const size_t es = dtype_size(d->expert_dtype);
@@ -270,7 +575,11 @@ so2_status so2conv_mix_experts_backward(const so2conv_mix_desc *d, int64_t n_sys
                    aligned_to(grad_experts, 16);
   if (grad_experts) {
     const dim3 grid((unsigned)ceil_div(n, vec ? 1024 : 256), (unsigned)(K < 4 ? K : 4));
-    if (vec)
+    if (!index && vec)
+      launch_rows<4>(K, (int)n_systems, n, weights, 1, k, grad_out, grad_experts, s);
+    else if (!index)
+      launch_rows<1>(K, (int)n_systems, n, weights, 1, k, grad_out, grad_experts, s);
+    else if (vec)
       k_mix_grad_experts<4><<<grid, 256, 0, s>>>(n_systems, K, k, n, weights, offsets, list,
                                                  grad_out, grad_experts);
     else
@@ -280,24 +589,17 @@ so2_status so2conv_mix_experts_backward(const so2conv_mix_desc *d, int64_t n_sys
   }
   if (grad_weights) {
     float *part = ws_at<float>(ws, p.part);
-    const dim3 grid(DOT_SPLITS, (unsigned)(slots < 4096 ? slots : 4096));
     typedef __nv_bfloat16 bf;
-    if (d->expert_dtype == SO2_F32) {
-      const float *x = static_cast<const float *>(experts);
-      if (vec)
-        k_mix_dots<4, float><<<grid, 256, 0, s>>>(slots, K, k, n, x, index, grad_out, part);
-      else
-        k_mix_dots<1, float><<<grid, 256, 0, s>>>(slots, K, k, n, x, index, grad_out, part);
-    } else {
-      const bf *x = static_cast<const bf *>(experts);
-      if (vec)
-        k_mix_dots<4, bf><<<grid, 256, 0, s>>>(slots, K, k, n, x, index, grad_out, part);
-      else
-        k_mix_dots<1, bf><<<grid, 256, 0, s>>>(slots, K, k, n, x, index, grad_out, part);
-    }
-    MODEL_CKL();
-    k_mix_dots_join<<<(unsigned)ceil_div(slots, 256), 256, 0, s>>>(slots, DOT_SPLITS, part,
-                                                                   grad_weights);
+    so2_status r2;
+    if (d->expert_dtype == SO2_F32)
+      r2 = vec ? mix_dots<true, float>(d, n_systems, p, experts, index, grad_out, part, s)
+               : mix_dots<false, float>(d, n_systems, p, experts, index, grad_out, part, s);
+    else
+      r2 = vec ? mix_dots<true, bf>(d, n_systems, p, experts, index, grad_out, part, s)
+               : mix_dots<false, bf>(d, n_systems, p, experts, index, grad_out, part, s);
+    if (r2 != SO2_OK) return r2;
+    k_mix_dots_join<<<(unsigned)ceil_div(slots, 8), 256, 0, s>>>(
+        slots, K, k, index, p.tiles, p.tiles ? n_systems * K : slots, p.splits, part, grad_weights);
     MODEL_CKL();
   }
   return SO2_OK;
