@@ -50,8 +50,8 @@ extern "C" {
  * id's rows are added in an order that depends on the sizes and the ids alone.
  *
  * Limits: 1 <= n_rows < 2^31 - 1, 1 <= channels <= 65,536, 1 <= n_comp <=
- * 1,024, 0 <= n <= 2^30; elements aligned.  grad_table must not overlap the
- * inputs.
+ * 1,024, 0 <= n <= 2^30, n * n_comp * channels <= 2^38; elements aligned.
+ * grad_table must not overlap the inputs.
  * -------------------------------------------------------------------------- */
 typedef struct {
   int64_t n_rows;
@@ -190,7 +190,7 @@ so2_status so2conv_mix_experts_backward(const so2conv_mix_desc *desc, int64_t n_
  * A dropped x is not used, so NaN there does not spread.  p = 1 drops all.
  *
  * Limits: 0 <= p <= 1, 1 <= channels <= 65,536, 1 <= n_comp <= 1,024, 0 <= n
- * <= 2^30, elements aligned.
+ * <= 2^30, n * n_comp * channels <= 2^38, elements aligned.
  * -------------------------------------------------------------------------- */
 enum { SO2_DROP_ELEMENT = 0, SO2_DROP_CHANNEL = 1, SO2_DROP_ROW = 2 };
 

@@ -367,7 +367,8 @@ so2_status so2conv_embed_forward(const so2conv_embed_desc *d, int64_t n, const i
   EmbedPlan p;
   so2_status r = embed_checks(d, n, ids, ws, ws_bytes, SO2_WS_FORWARD, p);
   if (r != SO2_OK) return r;
-  if (ld_out < (int64_t)d->n_comp * d->channels || ld_out > (1ll << 40)) return SO2_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)d->n_comp * d->channels;
+  if (ld_out < row || ld_out > (1ll << 40) || n > (1ll << 38) / row) return SO2_ERR_INVALID_ARG;
   if (n > 0 && (!table || !out || !aligned_to(table, dtype_size(d->table_dtype)) ||
                 !aligned_to(out, dtype_size(d->out_dtype))))
     return SO2_ERR_INVALID_ARG;
