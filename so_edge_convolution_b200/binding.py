@@ -159,7 +159,12 @@ def _c(t):
     return None if t is None else t.contiguous()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object
+
+
 def _stream(device):
+    if _raw_stream is not None and isinstance(device, torch.device) and device.index is not None:
+        return ctypes.c_void_p(_raw_stream(device.index))
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
@@ -501,13 +506,29 @@ def _model_ws(need, where, device, ws):
     return w.get(need)
 
 
+class _on:
+    """The tensors' device made current for a call, if it is another one."""
+
+    def __init__(self, device):
+        self.other = (torch.cuda.device(device)
+                      if torch.cuda.current_device() != device.index else None)
+
+    def __enter__(self):
+        if self.other is not None:
+            self.other.__enter__()
+
+    def __exit__(self, *exc):
+        if self.other is not None:
+            self.other.__exit__(*exc)
+
+
 def _need(t, name, shape, dtype, device=None):
     """`t`, contiguous, after a check of its shape, dtype and device."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, not {t.dtype} of "
                          f"shape {tuple(t.shape)}")
     _on_device(t, name, device)
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _on_device(t, name, device):
@@ -557,7 +578,7 @@ def embed_forward(desc, ids, table, out=None, ws=None):
     elif tuple(out.shape) != shape or out.dtype != dt or out.device != dev:
         raise ValueError(f"out must be {dt} of shape {shape} on {dev}")
     ld = _rows_of(out, n, desc.n_comp * desc.channels, "out")
-    with torch.cuda.device(dev):
+    with _on(dev):
         need = int(lib.so2conv_embed_workspace_size(ctypes.byref(desc), n, WS_FORWARD))
         p, nb = _model_ws(need, "embed_workspace_size", dev, ws)
         code = lib.so2conv_embed_forward(ctypes.byref(desc), n, _ptr(ids), _ptr(table),
@@ -586,7 +607,7 @@ def embed_backward(desc, ids, grad_out, out=None, ws=None):
         grad_out = grad_out.contiguous()
     ld = desc.channels if n <= 1 else grad_out.stride(0)
     out = _given_out(out, "out", (desc.n_rows, desc.channels), torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         need = int(lib.so2conv_embed_workspace_size(ctypes.byref(desc), n, WS_BACKWARD))
         p, nb = _model_ws(need, "embed_workspace_size", dev, ws)
         code = lib.so2conv_embed_backward(ctypes.byref(desc), n, _ptr(ids), grad_out.data_ptr(),
@@ -613,7 +634,7 @@ def route_forward(desc, logits, bias=None):
     weights = torch.empty((n, desc.top_k), dtype=torch.float32, device=dev)
     index = torch.empty((n, desc.top_k), dtype=torch.int32, device=dev)
     counts = torch.empty(desc.n_experts, dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         code = lib.so2conv_route_forward(ctypes.byref(desc), n, _ptr(logits), _ptr(bias),
                                          _ptr(weights), _ptr(index), _ptr(counts), _stream(dev))
     _check_call(code, "so2conv_route_forward")
@@ -629,7 +650,7 @@ def route_backward(desc, logits, index, grad_weights, out=None):
     index = _need(index, "index", (n, desc.top_k), torch.int32, dev)
     grad_weights = _need(grad_weights, "grad_weights", (n, desc.top_k), torch.float32, dev)
     out = _given_out(out, "out", (n, desc.n_experts), torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         code = lib.so2conv_route_backward(ctypes.byref(desc), n, _ptr(logits), _ptr(index),
                                           _ptr(grad_weights), _ptr(out), _stream(dev))
     _check_call(code, "so2conv_route_backward")
@@ -657,7 +678,7 @@ def mix_experts_forward(desc, experts, weights, index=None, out=None, ws=None):
     lib = load()
     n, dev, experts, weights, index = _mix_inputs(desc, experts, weights, index)
     out = _given_out(out, "out", (n, desc.n_weights), _torch_dtype(desc.out_dtype), dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         need = int(lib.so2conv_mix_workspace_size(ctypes.byref(desc), n, WS_FORWARD))
         p, nb = _model_ws(need, "mix_workspace_size", dev, ws)
         code = lib.so2conv_mix_experts_forward(ctypes.byref(desc), n, _ptr(experts),
@@ -678,7 +699,7 @@ def mix_experts_backward(desc, experts, weights, grad_out, index=None, need=None
     need = set(names if need is None else need)
     shapes = {"grad_experts": (desc.n_experts, desc.n_weights), "grad_weights": (n, desc.top_k)}
     outs = _outputs(names, need, shapes, out, dict(dtype=torch.float32, device=dev))
-    with torch.cuda.device(dev):
+    with _on(dev):
         size = int(lib.so2conv_mix_workspace_size(ctypes.byref(desc), n, WS_BACKWARD))
         p, nb = _model_ws(size, "mix_workspace_size", dev, ws)
         code = lib.so2conv_mix_experts_backward(ctypes.byref(desc), n, _ptr(experts),
@@ -708,7 +729,7 @@ def dropout(desc, x, rng, residual=None, rows=None, out=None):
     if rows is not None:
         rows = _need(rows, "rows", (n,), torch.int64, dev)
     out = _given_out(out, "out", shape, dt, dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         code = lib.so2conv_dropout(ctypes.byref(desc), n, _ptr(x), _ptr(residual), _ptr(rows),
                                    _ptr(rng), _ptr(out), _stream(dev))
     _check_call(code, "so2conv_dropout")
