@@ -3,35 +3,46 @@
 //
 // Backward.  The tokens are sorted by id (stable, least significant digit
 // first, 8 bits a pass), so that each id's rows are one run of the sorted
-// list.  The list is cut into equal ranges, one warp each; a warp adds its
-// rows in registers and writes every run that lies inside its range straight
-// to the table's gradient.  A run that crosses ranges leaves one partial sum
-// in each, which a second kernel adds in range order.  No atomics on floats:
-// the order of the additions depends on the sizes and the ids alone.
+// list.  The list is cut into equal ranges, one group of lanes each; a group
+// adds its rows in registers and writes every run that lies inside its range
+// straight to the table's gradient.  A run that crosses ranges leaves one
+// partial sum in each, which a second kernel adds in range order.  Few tokens
+// and a small table need no sort: a block per id scans the tokens.  No atomics
+// on floats: the order of the additions depends on the sizes and the ids alone.
 #include "model_common.cuh"
 
 namespace so2 {
 
 // ---- forward -----------------------------------------------------------------
-template <typename TT, typename TO>
+// A group of 2^shift lanes a node, V values a lane and step (V divides the
+// channels, so a vector is an element's row or zeros, not both).  The stores
+// bound it.  A grid of one block clears the status word itself.
+template <int V, typename TT, typename TO>
 __global__ void k_embed(int64_t n, const int64_t *__restrict__ ids, const TT *__restrict__ table,
                         int64_t n_rows, int channels, int64_t row, float scale, int64_t pad_id,
-                        TO *__restrict__ out, int64_t ld_out, DevStatus *st) {
-  const int64_t total = n * row;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t node = i / row, c = i - node * row;
-    float v = 0.f;
-    if (c < channels) {
-      const int64_t id = ids[node];
-      if (id != pad_id) {
-        if (id >= 0 && id < n_rows)
-          v = to_f32(table[id * channels + c]) * scale;
-        else
-          raise_error(st, SO2_ERR_INDEX, (int)(node & 0x7fffffff));
+                        TO *__restrict__ out, int64_t ld_out, int shift, DevStatus *st) {
+  if (gridDim.x == 1) {
+    if (threadIdx.x == 0) *st = DevStatus{0, 0};
+    __syncthreads();
+  }
+  const int64_t id0 = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  const int lane = (int)(id0 & ((1 << shift) - 1));
+  for (int64_t i = id0 >> shift; i < n; i += ((int64_t)gridDim.x * blockDim.x) >> shift) {
+    const int64_t id = ids[i];
+    const bool on = id != pad_id && id >= 0 && id < n_rows;
+    if (!on && id != pad_id && lane == 0) raise_error(st, SO2_ERR_INDEX, (int)(i & 0x7fffffff));
+    TO *o = out + i * ld_out;
+    for (int64_t c = (int64_t)lane * V; c < row; c += (int64_t)V << shift) {
+      float v[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[k] = 0.f;
+      if (on && c < channels) {
+        load_vec<V>(table + id * channels + c, v);
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] *= scale;
       }
+      store_vec<V>(o + c, v);
     }
-    out[node * ld_out + c] = from_f32<TO>(v);
   }
 }
 
@@ -50,25 +61,41 @@ __device__ __forceinline__ uint32_t embed_key(const int64_t *ids, int64_t i, int
   return (uint32_t)n_rows;
 }
 
-// hist[bin][block]: keys of the block's tile by digit.  FIRST reads the ids.
+// hist[bin][block]: keys of the block's tile by digit.  FIRST reads the ids,
+// clears the status word (the scatter records bad ids) and has its blocks
+// from nb on zero the table's gradient.
 template <bool FIRST>
 __global__ void k_sort_hist(int64_t n, const int64_t *__restrict__ ids, int64_t n_rows,
                             int64_t pad_id, const uint32_t *__restrict__ keys, int shift,
-                            uint32_t mask, int *__restrict__ hist, DevStatus *st) {
+                            uint32_t mask, int nb, int *__restrict__ hist,
+                            float *__restrict__ table, int64_t table_size, DevStatus *st) {
+  if (FIRST && blockIdx.x >= nb) {
+    const int64_t t = (blockIdx.x - nb) * (int64_t)SORT_THREADS + threadIdx.x;
+    const int64_t step = (int64_t)(gridDim.x - nb) * SORT_THREADS;
+    if ((reinterpret_cast<uintptr_t>(table) & 15) == 0) {
+      for (int64_t i = t; i < table_size / 4; i += step)
+        reinterpret_cast<float4 *>(table)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int64_t i = (table_size & ~3ll) + t; i < table_size; i += step) table[i] = 0.f;
+    } else {
+      for (int64_t i = t; i < table_size; i += step) table[i] = 0.f;
+    }
+    return;
+  }
   __shared__ int h[SORT_BINS];
+  if (FIRST && blockIdx.x == 0 && threadIdx.x == 0) *st = DevStatus{0, 0};
   h[threadIdx.x] = 0;
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * SORT_TILE;
-#pragma unroll 4
+#pragma unroll
   for (int r = 0; r < SORT_ROUNDS; ++r) {
     const int64_t i = t0 + r * SORT_THREADS + threadIdx.x;
     if (i < n) {
-      const uint32_t k = FIRST ? embed_key(ids, i, n_rows, pad_id, st) : keys[i];
+      const uint32_t k = FIRST ? embed_key(ids, i, n_rows, pad_id, nullptr) : keys[i];
       atomicAdd(&h[(k >> shift) & mask], 1);
     }
   }
   __syncthreads();
-  hist[(int64_t)threadIdx.x * gridDim.x + blockIdx.x] = h[threadIdx.x];
+  hist[(int64_t)threadIdx.x * nb + blockIdx.x] = h[threadIdx.x];
 }
 
 // Block-wide exclusive scan of one int per thread (256 threads); *total.
@@ -116,7 +143,8 @@ __global__ void k_sort_scatter(int64_t n, const int64_t *__restrict__ ids, int64
                                int64_t pad_id, const uint32_t *__restrict__ keys_in,
                                const int *__restrict__ perm_in, int shift, uint32_t mask,
                                const int *__restrict__ hist, const int *__restrict__ totals,
-                               uint32_t *__restrict__ keys_out, int *__restrict__ perm_out) {
+                               uint32_t *__restrict__ keys_out, int *__restrict__ perm_out,
+                               DevStatus *st) {
   __shared__ int cnt[SORT_WARPS][SORT_BINS];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
 #pragma unroll
@@ -129,7 +157,7 @@ __global__ void k_sort_scatter(int64_t n, const int64_t *__restrict__ ids, int64
     const int64_t i = t0 + r * 32 + lane;
     k[r] = 0xffffffffu;
     if (i < n) {
-      k[r] = FIRST ? embed_key(ids, i, n_rows, pad_id, nullptr) : keys_in[i];
+      k[r] = FIRST ? embed_key(ids, i, n_rows, pad_id, st) : keys_in[i];
       atomicAdd(&cnt[w][(k[r] >> shift) & mask], 1);
     }
   }
@@ -165,90 +193,180 @@ __global__ void k_sort_scatter(int64_t n, const int64_t *__restrict__ ids, int64
 }
 
 // ---- backward: sums of the runs --------------------------------------------------
-// One warp per range of `len` sorted tokens and slice of 32 * V channels.
-// head[r]: the range's share of a run that began before it; tail[r]: of a run
-// that begins in it and goes on after it.
+// One group of 2^shift lanes per range of `len` sorted tokens and slice of
+// V << shift channels.  head[r]: the range's share of a run that began before
+// it; tail[r]: of a run that begins in it and goes on after it.  Eight rows
+// are in flight a group; the next eight keys and places are read ahead.
+constexpr int RUN_ROWS = 8;  // divides len
+
 template <int V, typename TG>
-__global__ void k_embed_runs(int64_t n, int64_t n_ranges, int len,
-                             const uint32_t *__restrict__ keys, const int *__restrict__ perm,
-                             uint32_t n_rows, const TG *__restrict__ grad, int64_t ld, int channels,
-                             float scale, float *__restrict__ table, float *__restrict__ head,
-                             float *__restrict__ tail) {
-  const int lane = threadIdx.x & 31;
-  const int64_t r = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int c = (blockIdx.y * 32 + lane) * V;
-  if (r >= n_ranges) return;
+__global__ void __launch_bounds__(256)
+    k_embed_runs(int64_t n, int64_t n_ranges, int len, const uint32_t *__restrict__ keys,
+                 const int *__restrict__ perm, uint32_t n_rows, const TG *__restrict__ grad,
+                 int64_t ld, int channels, float scale, int shift, float *__restrict__ table,
+                 float *__restrict__ head, float *__restrict__ tail) {
+  const int64_t id = blockIdx.x * 256ll + threadIdx.x;
+  const int64_t r = id >> shift;
+  const int c = ((blockIdx.y << shift) + (int)(id & ((1 << shift) - 1))) * V;
+  if (r >= n_ranges || c >= channels) return;
   const int64_t a = r * len, b = a + len < n ? a + len : n;
   uint32_t cur = keys[a];
   if (cur >= n_rows) return;
-  const bool on = c < channels;
   bool from_before = a > 0 && keys[a - 1] == cur;
   float acc[V];
+  auto flush = [&](bool goes_on) {
+    if (from_before || goes_on) {
+      store_vec<V>((from_before ? head : tail) + r * channels + c, acc);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] *= scale;
+      store_vec<V>(table + (int64_t)cur * channels + c, acc);
+    }
+  };
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.f;
-  for (int64_t j = a; j < b; ++j) {
-    const uint32_t k = keys[j];
-    if (k != cur) {
-      if (on) {
-        if (from_before) {
-          store_vec<V>(head + r * channels + c, acc);
-        } else {
+  uint32_t k[RUN_ROWS], kn[RUN_ROWS];
+  int p[RUN_ROWS], pn[RUN_ROWS];
+  auto read = [&](int64_t j, uint32_t(&kk)[RUN_ROWS], int(&pp)[RUN_ROWS]) {
 #pragma unroll
-          for (int v = 0; v < V; ++v) acc[v] *= scale;
-          store_vec<V>(table + (int64_t)cur * channels + c, acc);
-        }
-      }
-      from_before = false;
-      cur = k;
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = 0.f;
-      if (cur >= n_rows) return;
+    for (int u = 0; u < RUN_ROWS; ++u) {
+      kk[u] = j + u < b ? keys[j + u] : 0xffffffffu;
+      pp[u] = j + u < b ? perm[j + u] : 0;
     }
-    if (on) {
-      float g[V];
-      load_vec<V>(grad + (int64_t)perm[j] * ld + c, g);
+  };
+  read(a, kn, pn);
+  for (int64_t j = a; j < b; j += RUN_ROWS) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += g[v];
+    for (int u = 0; u < RUN_ROWS; ++u) k[u] = kn[u], p[u] = pn[u];
+    float g[RUN_ROWS][V];
+#pragma unroll
+    for (int u = 0; u < RUN_ROWS; ++u)
+      if (k[u] < n_rows) load_vec<V>(grad + (int64_t)p[u] * ld + c, g[u]);
+    if (j + RUN_ROWS < b) read(j + RUN_ROWS, kn, pn);
+#pragma unroll
+    for (int u = 0; u < RUN_ROWS; ++u) {
+      if (k[u] != cur) {
+        if (j + u >= b) break;  // the list's end inside the last eight
+        flush(false);
+        from_before = false;
+        cur = k[u];
+        if (cur >= n_rows) return;  // tokens without a gradient end the list
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = 0.f;
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += g[u][v];
     }
   }
-  if (!on) return;
-  const bool goes_on = b < n && keys[b] == cur;
-  if (from_before) {
-    store_vec<V>(head + r * channels + c, acc);
-  } else if (goes_on) {
-    store_vec<V>(tail + r * channels + c, acc);
-  } else {
+  flush(b < n && keys[b] == cur);
+}
+
+// Runs that begin in one of the block's 32 ranges and go on after it: their
+// partial sums, warp w taking every eighth range from the w-th on.
+constexpr int JOIN_RANGES = 32;
+
+template <int V>
+__global__ void __launch_bounds__(256)
+    k_embed_join(int64_t n, int64_t n_ranges, int len, const uint32_t *__restrict__ keys,
+                 uint32_t n_rows, int channels, float scale, float *__restrict__ table,
+                 const float *__restrict__ head, const float *__restrict__ tail) {
+  __shared__ float part[8][32 * V];
+  __shared__ unsigned todo;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = (blockIdx.y * 32 + lane) * V;
+  const int64_t r0 = blockIdx.x * (int64_t)JOIN_RANGES;
+  if (w == 0) {
+    const int64_t a = (r0 + lane) * len, b = a + len;
+    bool begins = false;
+    if (b < n) {
+      const uint32_t key = keys[b - 1];
+      begins = key < n_rows && keys[b] == key && (a == 0 || keys[a - 1] != key);
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, begins);
+    if (lane == 0) todo = m;
+  }
+  __syncthreads();
+  for (unsigned m = todo; m; m &= m - 1) {
+    const int64_t r = r0 + __ffs(m) - 1;
+    const uint32_t key = keys[r * len + len - 1];
+    // the last range that starts inside the run
+    int64_t lo = r + 1, hi = n_ranges - 1;
+    while (lo < hi) {
+      const int64_t mid = (lo + hi + 1) >> 1;
+      if (keys[mid * len] == key) lo = mid;
+      else hi = mid - 1;
+    }
+    float acc[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] *= scale;
-    store_vec<V>(table + (int64_t)cur * channels + c, acc);
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    if (c < channels) {
+      if (w == 0) load_vec<V>(tail + r * channels + c, acc);
+#pragma unroll 4
+      for (int64_t q = r + 1 + w; q <= lo; q += 8) {
+        float g[V];
+        load_vec<V>(head + q * channels + c, g);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] += g[v];
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) part[w][lane * V + v] = acc[v];
+    __syncthreads();
+    if (w == 0 && c < channels) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += part[i][lane * V + v];
+        acc[v] = s * scale;
+      }
+      store_vec<V>(table + (int64_t)key * channels + c, acc);
+    }
+    __syncthreads();
   }
 }
 
-// One block per range: if a run begins in it and goes on after it, its
-// partial sums.  Eight warps take every eighth range of the run.
-template <int V>
-__global__ void k_embed_join(int64_t n, int64_t n_ranges, int len,
-                             const uint32_t *__restrict__ keys, uint32_t n_rows, int channels,
-                             float scale, float *__restrict__ table,
-                             const float *__restrict__ head, const float *__restrict__ tail) {
+// ---- backward: few tokens ------------------------------------------------------------
+// One block a table row and slice of 32 V channels: each of eight warps scans
+// an eighth of the ids and adds the rows that match, then the eight sums.
+template <int V, typename TG>
+__global__ void __launch_bounds__(256)
+    k_embed_scan(int n, const int64_t *__restrict__ ids, int64_t n_rows, int64_t pad_id,
+                 const TG *__restrict__ grad, int64_t ld, int channels, float scale,
+                 float *__restrict__ table, DevStatus *st) {
   __shared__ float part[8][32 * V];
-  const int64_t r = blockIdx.x;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t row = blockIdx.x;
   const int c = (blockIdx.y * 32 + lane) * V;
-  const int64_t a = r * len, b = a + len;
-  if (b >= n) return;
-  const uint32_t key = keys[b - 1];
-  if (key >= n_rows || keys[b] != key || (a > 0 && keys[a - 1] == key)) return;
+  const bool reports = row == 0 && blockIdx.y == 0;  // this block alone touches the status
+  if (reports) {
+    if (threadIdx.x == 0) *st = DevStatus{0, 0};
+    __syncthreads();
+  }
+  const int per = ((n + 255) / 256) * 32, i0 = w * per, i1 = i0 + per < n ? i0 + per : n;
   float acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.f;
-  if (c < channels) {
-    if (w == 0) load_vec<V>(tail + r * channels + c, acc);
-    for (int64_t q = r + 1 + w; q < n_ranges && keys[q * len] == key; q += 8) {
-      float g[V];
-      load_vec<V>(head + q * channels + c, g);
+  for (int i = i0; i < i1; i += 32) {
+    const int64_t id = i + lane < i1 ? ids[i + lane] : pad_id;
+    const bool bad = id != pad_id && (id < 0 || id >= n_rows);
+    if (reports && bad) raise_error(st, SO2_ERR_INDEX, i + lane);
+    unsigned m = __ballot_sync(0xffffffffu, i + lane < i1 && id == row && id != pad_id);
+    if (c >= channels) continue;
+    while (m) {  // four rows in flight
+      float g[4][V];
+      int j[4];
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += g[v];
+      for (int u = 0; u < 4; ++u) {
+        j[u] = m ? i + __ffs(m) - 1 : -1;
+        m &= m - 1;
+        if (j[u] >= 0) load_vec<V>(grad + (int64_t)j[u] * ld + c, g[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (j[u] >= 0)
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] += g[u][v];
     }
   }
 #pragma unroll
@@ -262,7 +380,7 @@ __global__ void k_embed_join(int64_t n, int64_t n_ranges, int len,
       for (int i = 0; i < 8; ++i) s += part[i][lane * V + v];
       acc[v] = s * scale;
     }
-    store_vec<V>(table + (int64_t)key * channels + c, acc);
+    store_vec<V>(table + row * channels + c, acc);
   }
 }
 
@@ -283,19 +401,32 @@ bool embed_ok(const so2conv_embed_desc *d) {
          d->n_comp >= 1 && d->n_comp <= 1024 && dtype_ok(d->table_dtype) && dtype_ok(d->out_dtype);
 }
 
+// Tokens few enough that every table row looks at all of them: the scans are
+// n_rows * n / 32 steps of a warp, and a row's own tokens one eighth of n deep
+// at worst.  It is one launch where the sort takes six.
+bool embed_scans(const so2conv_embed_desc *d, int64_t n) {
+  return n <= 2048 && d->n_rows * n <= (1 << 20);
+}
+
+// Lanes that take a row of `vectors` vectors, as a power of two.
+int lane_shift(int64_t vectors) {
+  int s = 0;
+  while (s < 5 && (1 << s) < vectors) ++s;
+  return s;
+}
+
 EmbedPlan embed_plan(const so2conv_embed_desc *d, int64_t n, int which) {
   EmbedPlan p{};
   size_t c = 0;
   p.status = ws_take(c, sizeof(DevStatus));
-  if (which == SO2_WS_BACKWARD && n > 0) {
+  if (which == SO2_WS_BACKWARD && n > 0 && !embed_scans(d, n)) {
     int bits = 1;  // of the keys 0..n_rows
     while ((d->n_rows >> bits) != 0) ++bits;
     p.passes = (bits + 7) / 8;
     p.bits = (bits + p.passes - 1) / p.passes;
     p.nb = (int)ceil_div(n, SORT_TILE);
-    // about 32 warps of ranges for each SM, of 8 tokens at least
-    const int64_t len = ceil_div(n, MODEL_SMS * 32);
-    p.len = (int)(len < 8 ? 8 : len);
+    // about 32 warps of ranges for each SM
+    p.len = (int)(ceil_div(ceil_div(n, MODEL_SMS * 32), RUN_ROWS) * RUN_ROWS);
     p.n_ranges = ceil_div(n, p.len);
     for (int i = 0; i < 2; ++i) {
       p.keys[i] = ws_take(c, sizeof(uint32_t) * n);
@@ -321,33 +452,106 @@ so2_status embed_checks(const so2conv_embed_desc *d, int64_t n, const int64_t *i
   return SO2_OK;
 }
 
-template <typename TT, typename TO>
-void launch_embed(const so2conv_embed_desc *d, int64_t n, const int64_t *ids, const void *table,
-                  void *out, int64_t ld, DevStatus *st, cudaStream_t s) {
+template <int V, typename TT, typename TO>
+so2_status launch_embed(const so2conv_embed_desc *d, int64_t n, const int64_t *ids, const TT *table,
+                        TO *out, int64_t ld, DevStatus *st, cudaStream_t s) {
   const int64_t row = (int64_t)d->n_comp * d->channels;
-  const int64_t want = ceil_div(n * row, 256);
-  const int grid = (int)(want < MODEL_SMS * 16 ? want : MODEL_SMS * 16);
-  k_embed<TT, TO><<<grid, 256, 0, s>>>(n, ids, static_cast<const TT *>(table), d->n_rows,
-                                       d->channels, row, d->scale, d->pad_id,
-                                       static_cast<TO *>(out), ld, st);
+  const int shift = lane_shift(row / V);
+  // one block, without a clearing launch before it, for what it does at once
+  const bool one = n * row / V <= 4096;
+  if (!one) MODEL_CK(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
+  const int threads = one ? 1024 : 256;
+  int64_t grid = one ? 1 : ceil_div(n << shift, threads);
+  if (grid > 0x7fffffff) grid = 0x7fffffff;
+  k_embed<V, TT, TO><<<(unsigned)grid, threads, 0, s>>>(n, ids, table, d->n_rows, d->channels, row,
+                                                        d->scale, d->pad_id, out, ld, shift, st);
+  MODEL_CKL();
+  return SO2_OK;
+}
+
+template <typename TT, typename TO>
+so2_status launch_embed(const so2conv_embed_desc *d, int64_t n, const int64_t *ids,
+                        const void *table, void *out, int64_t ld, DevStatus *st, cudaStream_t s) {
+  constexpr int V = 16 / (int)sizeof(TO);  // 16-byte stores where every row allows them
+  const TT *t = static_cast<const TT *>(table);
+  TO *o = static_cast<TO *>(out);
+  if (d->channels % V == 0 && ld % V == 0 && aligned_to(out, 16) &&
+      aligned_to(table, V * sizeof(TT) < 16 ? V * sizeof(TT) : 16))
+    return launch_embed<V>(d, n, ids, t, o, ld, st, s);
+  return launch_embed<1>(d, n, ids, t, o, ld, st, s);
 }
 
 template <int V, typename TG>
 so2_status embed_sums(const so2conv_embed_desc *d, int64_t n, const EmbedPlan &p, void *ws,
-                      const uint32_t *keys, const int *perm, const void *grad, int64_t ld,
+                      const uint32_t *keys, const int *perm, const TG *grad, int64_t ld,
                       float *table, cudaStream_t s) {
-  const int slices = (int)ceil_div(d->channels, 32 * V);
+  const int shift = lane_shift(ceil_div(d->channels, V));
   float *head = ws_at<float>(ws, p.head), *tail = ws_at<float>(ws, p.tail);
-  k_embed_runs<V, TG><<<dim3((unsigned)ceil_div(p.n_ranges, 8), slices), 256, 0, s>>>(
-      n, p.n_ranges, p.len, keys, perm, (uint32_t)d->n_rows, static_cast<const TG *>(grad), ld,
-      d->channels, d->scale, table, head, tail);
+  const dim3 grid((unsigned)ceil_div(p.n_ranges << shift, 256),
+                  (unsigned)ceil_div(d->channels, (int64_t)V << shift));
+  k_embed_runs<V, TG><<<grid, 256, 0, s>>>(n, p.n_ranges, p.len, keys, perm, (uint32_t)d->n_rows,
+                                           grad, ld, d->channels, d->scale, shift, table, head, tail);
   MODEL_CKL();
   if (p.n_ranges > 1) {
-    k_embed_join<V><<<dim3((unsigned)p.n_ranges, slices), 256, 0, s>>>(
-        n, p.n_ranges, p.len, keys, (uint32_t)d->n_rows, d->channels, d->scale, table, head, tail);
+    const dim3 g2((unsigned)ceil_div(p.n_ranges, JOIN_RANGES), (unsigned)ceil_div(d->channels, 32 * V));
+    k_embed_join<V><<<g2, 256, 0, s>>>(n, p.n_ranges, p.len, keys, (uint32_t)d->n_rows, d->channels,
+                                       d->scale, table, head, tail);
     MODEL_CKL();
   }
   return SO2_OK;
+}
+
+template <int V, typename TG>
+so2_status embed_grad(const so2conv_embed_desc *d, int64_t n, const int64_t *ids, const EmbedPlan &p,
+                      void *ws, const TG *grad, int64_t ld, float *table, cudaStream_t s) {
+  DevStatus *st = ws_at<DevStatus>(ws, p.status);
+  if (embed_scans(d, n)) {
+    const dim3 grid((unsigned)d->n_rows, (unsigned)ceil_div(d->channels, 32 * V));
+    k_embed_scan<V, TG><<<grid, 256, 0, s>>>((int)n, ids, d->n_rows, d->pad_id, grad, ld,
+                                             d->channels, d->scale, table, st);
+    MODEL_CKL();
+    return SO2_OK;
+  }
+  int *hist = ws_at<int>(ws, p.hist), *totals = ws_at<int>(ws, p.totals);
+  const uint32_t mask = (1u << p.bits) - 1;
+  const int64_t size = d->n_rows * d->channels;
+  const int64_t zeroing = ceil_div(size, SORT_THREADS * 16);
+  const unsigned extra = (unsigned)(zeroing < MODEL_SMS * 8 ? zeroing : MODEL_SMS * 8);
+  for (int q = 0; q < p.passes; ++q) {
+    const uint32_t *ki = ws_at<uint32_t>(ws, p.keys[(q + 1) & 1]);
+    const int *pi = ws_at<int>(ws, p.perm[(q + 1) & 1]);
+    uint32_t *ko = ws_at<uint32_t>(ws, p.keys[q & 1]);
+    int *po = ws_at<int>(ws, p.perm[q & 1]);
+    const int shift = q * p.bits;
+    if (q == 0)
+      k_sort_hist<true><<<p.nb + extra, SORT_THREADS, 0, s>>>(
+          n, ids, d->n_rows, d->pad_id, nullptr, shift, mask, p.nb, hist, table, size, st);
+    else
+      k_sort_hist<false><<<p.nb, SORT_THREADS, 0, s>>>(n, nullptr, 0, 0, ki, shift, mask, p.nb, hist,
+                                                       nullptr, 0, st);
+    MODEL_CKL();
+    k_sort_scan<<<SORT_BINS, SORT_THREADS, 0, s>>>(p.nb, hist, totals);
+    MODEL_CKL();
+    if (q == 0)
+      k_sort_scatter<true><<<p.nb, SORT_THREADS, 0, s>>>(n, ids, d->n_rows, d->pad_id, nullptr,
+                                                         nullptr, shift, mask, hist, totals, ko, po, st);
+    else
+      k_sort_scatter<false><<<p.nb, SORT_THREADS, 0, s>>>(n, nullptr, 0, 0, ki, pi, shift, mask,
+                                                          hist, totals, ko, po, st);
+    MODEL_CKL();
+  }
+  return embed_sums<V, TG>(d, n, p, ws, ws_at<uint32_t>(ws, p.keys[(p.passes + 1) & 1]),
+                           ws_at<int>(ws, p.perm[(p.passes + 1) & 1]), grad, ld, table, s);
+}
+
+template <typename TG>
+so2_status embed_grad(const so2conv_embed_desc *d, int64_t n, const int64_t *ids, const EmbedPlan &p,
+                      void *ws, const void *grad, int64_t ld, float *table, cudaStream_t s) {
+  const TG *g = static_cast<const TG *>(grad);
+  // rows in vectors of four where every row starts on one's boundary
+  if (d->channels % 4 == 0 && ld % 4 == 0 && aligned_to(grad, 4 * sizeof(TG)) && aligned_to(table, 16))
+    return embed_grad<4, TG>(d, n, ids, p, ws, g, ld, table, s);
+  return embed_grad<1, TG>(d, n, ids, p, ws, g, ld, table, s);
 }
 
 }  // namespace
@@ -374,19 +578,18 @@ so2_status so2conv_embed_forward(const so2conv_embed_desc *d, int64_t n, const i
     return SO2_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DevStatus *st = ws_at<DevStatus>(ws, p.status);
-  MODEL_CK(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
-  if (n == 0) return SO2_OK;
+  if (n == 0) {
+    MODEL_CK(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
+    return SO2_OK;
+  }
   typedef __nv_bfloat16 bf;
   if (d->table_dtype == SO2_F32 && d->out_dtype == SO2_F32)
-    launch_embed<float, float>(d, n, ids, table, out, ld_out, st, s);
-  else if (d->table_dtype == SO2_F32)
-    launch_embed<float, bf>(d, n, ids, table, out, ld_out, st, s);
-  else if (d->out_dtype == SO2_F32)
-    launch_embed<bf, float>(d, n, ids, table, out, ld_out, st, s);
-  else
-    launch_embed<bf, bf>(d, n, ids, table, out, ld_out, st, s);
-  MODEL_CKL();
-  return SO2_OK;
+    return launch_embed<float, float>(d, n, ids, table, out, ld_out, st, s);
+  if (d->table_dtype == SO2_F32)
+    return launch_embed<float, bf>(d, n, ids, table, out, ld_out, st, s);
+  if (d->out_dtype == SO2_F32)
+    return launch_embed<bf, float>(d, n, ids, table, out, ld_out, st, s);
+  return launch_embed<bf, bf>(d, n, ids, table, out, ld_out, st, s);
 }
 
 so2_status so2conv_embed_backward(const so2conv_embed_desc *d, int64_t n, const int64_t *ids,
@@ -400,44 +603,14 @@ so2_status so2conv_embed_backward(const so2conv_embed_desc *d, int64_t n, const 
   const size_t es = dtype_size(d->out_dtype);
   if (n > 0 && (!grad_out || !aligned_to(grad_out, es))) return SO2_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  DevStatus *st = ws_at<DevStatus>(ws, p.status);
-  MODEL_CK(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
-  MODEL_CK(cudaMemsetAsync(grad_table, 0, sizeof(float) * d->n_rows * d->channels, s));
-  if (n == 0) return SO2_OK;
-  int *hist = ws_at<int>(ws, p.hist), *totals = ws_at<int>(ws, p.totals);
-  const uint32_t mask = (1u << p.bits) - 1;
-  for (int q = 0; q < p.passes; ++q) {
-    const uint32_t *ki = ws_at<uint32_t>(ws, p.keys[(q + 1) & 1]);
-    const int *pi = ws_at<int>(ws, p.perm[(q + 1) & 1]);
-    uint32_t *ko = ws_at<uint32_t>(ws, p.keys[q & 1]);
-    int *po = ws_at<int>(ws, p.perm[q & 1]);
-    const int shift = q * p.bits;
-    if (q == 0)
-      k_sort_hist<true><<<p.nb, SORT_THREADS, 0, s>>>(n, ids, d->n_rows, d->pad_id, nullptr, shift,
-                                                      mask, hist, st);
-    else
-      k_sort_hist<false><<<p.nb, SORT_THREADS, 0, s>>>(n, nullptr, 0, 0, ki, shift, mask, hist, st);
-    MODEL_CKL();
-    k_sort_scan<<<SORT_BINS, SORT_THREADS, 0, s>>>(p.nb, hist, totals);
-    MODEL_CKL();
-    if (q == 0)
-      k_sort_scatter<true><<<p.nb, SORT_THREADS, 0, s>>>(n, ids, d->n_rows, d->pad_id, nullptr,
-                                                         nullptr, shift, mask, hist, totals, ko, po);
-    else
-      k_sort_scatter<false><<<p.nb, SORT_THREADS, 0, s>>>(n, nullptr, 0, 0, ki, pi, shift, mask,
-                                                          hist, totals, ko, po);
-    MODEL_CKL();
+  if (n == 0) {
+    MODEL_CK(cudaMemsetAsync(ws_at<DevStatus>(ws, p.status), 0, sizeof(DevStatus), s));
+    MODEL_CK(cudaMemsetAsync(grad_table, 0, sizeof(float) * d->n_rows * d->channels, s));
+    return SO2_OK;
   }
-  const uint32_t *keys = ws_at<uint32_t>(ws, p.keys[(p.passes + 1) & 1]);
-  const int *perm = ws_at<int>(ws, p.perm[(p.passes + 1) & 1]);
-  // rows in vectors of four where every row starts on one's boundary
-  const bool vec = d->channels % 4 == 0 && ld_grad % 4 == 0 && aligned_to(grad_out, 4 * es) &&
-                   aligned_to(grad_table, 16);
   if (d->out_dtype == SO2_F32)
-    return vec ? embed_sums<4, float>(d, n, p, ws, keys, perm, grad_out, ld_grad, grad_table, s)
-               : embed_sums<1, float>(d, n, p, ws, keys, perm, grad_out, ld_grad, grad_table, s);
-  return vec ? embed_sums<4, __nv_bfloat16>(d, n, p, ws, keys, perm, grad_out, ld_grad, grad_table, s)
-             : embed_sums<1, __nv_bfloat16>(d, n, p, ws, keys, perm, grad_out, ld_grad, grad_table, s);
+    return embed_grad<float>(d, n, ids, p, ws, grad_out, ld_grad, grad_table, s);
+  return embed_grad<__nv_bfloat16>(d, n, ids, p, ws, grad_out, ld_grad, grad_table, s);
 }
 
 }  // extern "C"
