@@ -48,7 +48,7 @@ __global__ void k_embed(int64_t n, const int64_t *__restrict__ ids, const TT *__
 
 // ---- backward: sort ------------------------------------------------------------
 constexpr int SORT_THREADS = 256, SORT_WARPS = 8;
-constexpr int SORT_ROUNDS = 16;                          // 32 keys of a warp each
+constexpr int SORT_ROUNDS = 4;                           // 32 keys of a warp each
 constexpr int SORT_TILE = SORT_THREADS * SORT_ROUNDS;    // keys of a block
 constexpr int SORT_BINS = 256;
 
@@ -89,10 +89,14 @@ __global__ void k_sort_hist(int64_t n, const int64_t *__restrict__ ids, int64_t 
 #pragma unroll
   for (int r = 0; r < SORT_ROUNDS; ++r) {
     const int64_t i = t0 + r * SORT_THREADS + threadIdx.x;
+    uint32_t d = SORT_BINS;
     if (i < n) {
       const uint32_t k = FIRST ? embed_key(ids, i, n_rows, pad_id, nullptr) : keys[i];
-      atomicAdd(&h[(k >> shift) & mask], 1);
+      d = (k >> shift) & mask;
     }
+    // one addition for the lanes of a warp that share a digit
+    const unsigned same = __match_any_sync(0xffffffffu, d);
+    if (d < SORT_BINS && (threadIdx.x & 31) == __ffs(same) - 1) atomicAdd(&h[d], __popc(same));
   }
   __syncthreads();
   hist[(int64_t)threadIdx.x * nb + blockIdx.x] = h[threadIdx.x];
@@ -136,35 +140,50 @@ __global__ void k_sort_scan(int nb, int *__restrict__ hist, int *__restrict__ to
   if (threadIdx.x == 0) totals[blockIdx.x] = carry;
 }
 
-// Stable scatter of the tile: a warp's 512 keys are consecutive, so the order
-// inside the tile is (warp, round, lane).
+// Stable scatter of the tile: a warp's 128 keys are consecutive, so the order
+// inside the tile is (warp, round, lane).  A key's rank among its warp's equal
+// digits comes from matching the lanes; the warps' counts and the blocks'
+// sums then place it.
 template <bool FIRST>
-__global__ void k_sort_scatter(int64_t n, const int64_t *__restrict__ ids, int64_t n_rows,
-                               int64_t pad_id, const uint32_t *__restrict__ keys_in,
-                               const int *__restrict__ perm_in, int shift, uint32_t mask,
-                               const int *__restrict__ hist, const int *__restrict__ totals,
-                               uint32_t *__restrict__ keys_out, int *__restrict__ perm_out,
-                               DevStatus *st) {
-  __shared__ int cnt[SORT_WARPS][SORT_BINS];
+__global__ void __launch_bounds__(SORT_THREADS)
+    k_sort_scatter(int64_t n, const int64_t *__restrict__ ids, int64_t n_rows, int64_t pad_id,
+                   const uint32_t *__restrict__ keys_in, const int *__restrict__ perm_in, int shift,
+                   uint32_t mask, const int *__restrict__ hist, const int *__restrict__ totals,
+                   uint32_t *__restrict__ keys_out, int *__restrict__ perm_out, DevStatus *st) {
+  __shared__ int cnt[SORT_WARPS][SORT_BINS + 1];  // the last one takes lanes beyond the list
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-#pragma unroll
-  for (int i = 0; i < SORT_WARPS; ++i) cnt[i][tid] = 0;
-  __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * SORT_TILE + w * (32 * SORT_ROUNDS);
-  uint32_t k[SORT_ROUNDS];
+  uint32_t k[SORT_ROUNDS], d[SORT_ROUNDS];
+  int p[SORT_ROUNDS], rank[SORT_ROUNDS];
 #pragma unroll
   for (int r = 0; r < SORT_ROUNDS; ++r) {
     const int64_t i = t0 + r * 32 + lane;
-    k[r] = 0xffffffffu;
+    k[r] = 0;
+    p[r] = (int)i;
     if (i < n) {
       k[r] = FIRST ? embed_key(ids, i, n_rows, pad_id, st) : keys_in[i];
-      atomicAdd(&cnt[w][(k[r] >> shift) & mask], 1);
+      if (!FIRST) p[r] = perm_in[i];
     }
+    d[r] = i < n ? (k[r] >> shift) & mask : SORT_BINS;
+  }
+  const int before = hist[(int64_t)tid * gridDim.x + blockIdx.x], total = totals[tid];
+#pragma unroll
+  for (int i = 0; i < SORT_WARPS; ++i) cnt[i][tid] = 0;
+  if (tid < SORT_WARPS) cnt[tid][SORT_BINS] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < SORT_ROUNDS; ++r) {
+    const unsigned same = __match_any_sync(0xffffffffu, d[r]);
+    const int ahead = __popc(same & ((1u << lane) - 1));
+    rank[r] = cnt[w][d[r]] + ahead;
+    __syncwarp();
+    if (ahead == 0) cnt[w][d[r]] += __popc(same);
+    __syncwarp();
   }
   int unused;
-  const int first = block_scan256(totals[tid], &unused);  // synchronises the block
+  const int first = block_scan256(total, &unused);  // synchronises the block
   {
-    int s = first + hist[(int64_t)tid * gridDim.x + blockIdx.x];
+    int s = first + before;
 #pragma unroll
     for (int i = 0; i < SORT_WARPS; ++i) {
       const int c = cnt[i][tid];
@@ -174,22 +193,12 @@ __global__ void k_sort_scatter(int64_t n, const int64_t *__restrict__ ids, int64
   }
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < SORT_ROUNDS; ++r) {
-    const int64_t i = t0 + r * 32 + lane;
-    const bool in = i < n;
-    const uint32_t d = in ? (k[r] >> shift) & mask : SORT_BINS;
-    const unsigned same = __match_any_sync(0xffffffffu, d);
-    const int rank = __popc(same & ((1u << lane) - 1));
-    int at = 0;
-    if (in) at = cnt[w][d] + rank;
-    __syncwarp();
-    if (in && rank == 0) cnt[w][d] += __popc(same);
-    __syncwarp();
-    if (in) {
+  for (int r = 0; r < SORT_ROUNDS; ++r)
+    if (t0 + r * 32 + lane < n) {
+      const int at = cnt[w][d[r]] + rank[r];
       keys_out[at] = k[r];
-      perm_out[at] = FIRST ? (int)i : perm_in[i];
+      perm_out[at] = p[r];
     }
-  }
 }
 
 // ---- backward: sums of the runs --------------------------------------------------
@@ -262,52 +271,78 @@ __global__ void __launch_bounds__(256)
 }
 
 // Runs that begin in one of the block's 32 ranges and go on after it: their
-// partial sums, warp w taking every eighth range from the w-th on.
-constexpr int JOIN_RANGES = 32;
+// partial sums in range order.  A short run is one warp's, all warps taking
+// runs of their own; a long one is the whole block's, warp w adding every
+// sixteenth range from the w-th on.
+constexpr int JOIN_RANGES = 32, JOIN_WARPS = 16, JOIN_ALONE = 32;
 
 template <int V>
-__global__ void __launch_bounds__(256)
+__device__ __forceinline__ void join_add(float (&acc)[V], const float *from) {
+  float g[V];
+  load_vec<V>(from, g);
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] += g[v];
+}
+
+template <int V>
+__global__ void __launch_bounds__(32 * JOIN_WARPS)
     k_embed_join(int64_t n, int64_t n_ranges, int len, const uint32_t *__restrict__ keys,
                  uint32_t n_rows, int channels, float scale, float *__restrict__ table,
                  const float *__restrict__ head, const float *__restrict__ tail) {
-  __shared__ float part[8][32 * V];
-  __shared__ unsigned todo;
+  __shared__ float part[JOIN_WARPS][32 * V];
+  __shared__ int64_t last[JOIN_RANGES];  // of long runs: the last range that starts in it
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = (blockIdx.y * 32 + lane) * V;
   const int64_t r0 = blockIdx.x * (int64_t)JOIN_RANGES;
-  if (w == 0) {
+  unsigned todo;
+  {  // every warp looks for itself
     const int64_t a = (r0 + lane) * len, b = a + len;
     bool begins = false;
     if (b < n) {
       const uint32_t key = keys[b - 1];
       begins = key < n_rows && keys[b] == key && (a == 0 || keys[a - 1] != key);
     }
-    const unsigned m = __ballot_sync(0xffffffffu, begins);
-    if (lane == 0) todo = m;
+    todo = __ballot_sync(0xffffffffu, begins);
+  }
+  if (w == 0) last[lane] = -1;
+  __syncthreads();
+  int nth = 0;
+  for (unsigned m = todo; m; m &= m - 1, ++nth) {
+    if (nth % JOIN_WARPS != w) continue;
+    const int64_t r = r0 + __ffs(m) - 1;
+    const uint32_t key = keys[r * len + len - 1];
+    int64_t lo = r + 1, hi = n_ranges - 1;
+    while (lo < hi) {  // 32 probes a step
+      const int64_t step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+      const bool in = at <= hi && keys[at * len] == key;
+      const int hits = __popc(__ballot_sync(0xffffffffu, in));
+      const int64_t end = lo + (hits + 1) * step - 1;
+      lo += hits * step;
+      hi = end < hi ? end : hi;
+    }
+    if (lo - r > JOIN_ALONE) {
+      if (lane == 0) last[r - r0] = lo;
+    } else if (c < channels) {
+      float acc[V];
+      load_vec<V>(tail + r * channels + c, acc);
+#pragma unroll 4
+      for (int64_t q = r + 1; q <= lo; ++q) join_add<V>(acc, head + q * channels + c);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] *= scale;
+      store_vec<V>(table + (int64_t)key * channels + c, acc);
+    }
   }
   __syncthreads();
   for (unsigned m = todo; m; m &= m - 1) {
-    const int64_t r = r0 + __ffs(m) - 1;
-    const uint32_t key = keys[r * len + len - 1];
-    // the last range that starts inside the run
-    int64_t lo = r + 1, hi = n_ranges - 1;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi + 1) >> 1;
-      if (keys[mid * len] == key) lo = mid;
-      else hi = mid - 1;
-    }
+    const int64_t r = r0 + __ffs(m) - 1, lo = last[r - r0];
+    if (lo < 0) continue;
     float acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
     if (c < channels) {
       if (w == 0) load_vec<V>(tail + r * channels + c, acc);
-#pragma unroll 4
-      for (int64_t q = r + 1 + w; q <= lo; q += 8) {
-        float g[V];
-        load_vec<V>(head + q * channels + c, g);
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] += g[v];
-      }
+#pragma unroll 8
+      for (int64_t q = r + 1 + w; q <= lo; q += JOIN_WARPS) join_add<V>(acc, head + q * channels + c);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) part[w][lane * V + v] = acc[v];
@@ -317,10 +352,10 @@ __global__ void __launch_bounds__(256)
       for (int v = 0; v < V; ++v) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += part[i][lane * V + v];
+        for (int i = 0; i < JOIN_WARPS; ++i) s += part[i][lane * V + v];
         acc[v] = s * scale;
       }
-      store_vec<V>(table + (int64_t)key * channels + c, acc);
+      store_vec<V>(table + (int64_t)keys[r * len + len - 1] * channels + c, acc);
     }
     __syncthreads();
   }
@@ -427,6 +462,7 @@ EmbedPlan embed_plan(const so2conv_embed_desc *d, int64_t n, int which) {
     p.nb = (int)ceil_div(n, SORT_TILE);
     // about 32 warps of ranges for each SM
     p.len = (int)(ceil_div(ceil_div(n, MODEL_SMS * 32), RUN_ROWS) * RUN_ROWS);
+    if (p.len < 2 * RUN_ROWS) p.len = 2 * RUN_ROWS;
     p.n_ranges = ceil_div(n, p.len);
     for (int i = 0; i < 2; ++i) {
       p.keys[i] = ws_take(c, sizeof(uint32_t) * n);
@@ -494,7 +530,7 @@ so2_status embed_sums(const so2conv_embed_desc *d, int64_t n, const EmbedPlan &p
   MODEL_CKL();
   if (p.n_ranges > 1) {
     const dim3 g2((unsigned)ceil_div(p.n_ranges, JOIN_RANGES), (unsigned)ceil_div(d->channels, 32 * V));
-    k_embed_join<V><<<g2, 256, 0, s>>>(n, p.n_ranges, p.len, keys, (uint32_t)d->n_rows, d->channels,
+    k_embed_join<V><<<g2, 32 * JOIN_WARPS, 0, s>>>(n, p.n_ranges, p.len, keys, (uint32_t)d->n_rows, d->channels,
                                        d->scale, table, head, tail);
     MODEL_CKL();
   }
