@@ -1,9 +1,13 @@
 // route.cu -- routing to experts: scores, selection and the logits' gradient.
 //
-// One warp per token.  Experts are ranked by a 64-bit key in the order of
+// One warp per token.  Experts are ranked by an integer key in the order of
 // their selection scores: 0 for an expert that may not be chosen, 1 for NaN,
-// then the numbers.  Without a bias the logits themselves give the order;
-// with one, c = s + bias is formed in 64 bits.
+// then the numbers.  Without a bias the logits themselves give the order, in
+// 32 bits exactly.  With one (or ranks of groups by two scores), c = s + bias
+// is formed in f32 first, and a row in which two scores that meet at a place
+// of the order lie closer than f32 can tell is ranked again in 64 bits.  That
+// is rare (two scores within 2^-20 of each other), so the order of 64 bits
+// costs what the order of f32 does.
 #include <math.h>
 
 #include "model_common.cuh"
@@ -39,110 +43,212 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// The largest key of the warp and the lowest index that has it.
-__device__ __forceinline__ void warp_best(uint64_t &key, int &idx) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const uint64_t k = __shfl_xor_sync(0xffffffffu, key, o);
-    const int i = __shfl_xor_sync(0xffffffffu, idx, o);
-    if (k > key || (k == key && i < idx)) key = k, idx = i;
-  }
-}
-
 __device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + expf(-x)); }
 
 constexpr int ROUTE_WARPS = 4;
 
-// Shared memory per warp: keys [K] u64, chosen [top_k] f32, group keys [n_groups] u64.
-template <int NPL, typename T>  // NPL experts a lane: e = lane + 32 i
-__global__ void k_route(RouteArgs a, int64_t n, const T *__restrict__ logits,
-                        const float *__restrict__ bias, float *__restrict__ weights,
-                        int *__restrict__ index, int *__restrict__ counts) {
+// The order of a row by scores in 64 bits: rank[e] is K for the first expert
+// down to 1, or 0 if it may not be chosen.  All lanes of the warp call; keys
+// (K + n_groups words) and rank (K words) are the warp's shared memory, and
+// nothing of the caller's is passed in registers, so that the usual path does
+// not pay for this one.
+template <typename T>
+__device__ __noinline__ void rank_in_64_bits(const RouteArgs &a, const T *__restrict__ row, float m0,
+                                             const float *__restrict__ bias, uint64_t *keys,
+                                             uint32_t *rank) {
+  const int lane = threadIdx.x & 31;
+  uint64_t *gkeys = keys + a.K;
+  double *cs = reinterpret_cast<double *>(keys);
+  __syncwarp();
+  double z = 0.0;
+  if (a.softmax) {
+    for (int e = lane; e < a.K; e += 32) z += exp((double)to_f32(row[e]) - m0);
+    z = warp_sum(z);
+  }
+  for (int e = lane; e < a.K; e += 32) {
+    const double x = to_f32(row[e]);
+    double c = a.softmax ? exp(x - m0) / z : 1.0 / (1.0 + exp(-x));
+    if (bias) c += bias[e];
+    cs[e] = x == -INFINITY ? -INFINITY : c;
+  }
+  __syncwarp();
+  const bool grouped = a.top_groups < a.n_groups;
+  for (int g = lane; grouped && g < a.n_groups; g += 32) {
+    double b0 = -INFINITY, b1 = -INFINITY;
+    bool nan = false;
+    for (int j = 0; j < a.per; ++j) {
+      const double c = cs[g * a.per + j];
+      if (c != c) nan = true;
+      else if (c > b0) b1 = b0, b0 = c;
+      else if (c > b1) b1 = c;
+    }
+    // NaN ranks below every number: it counts where too few numbers are left
+    const bool two = a.group_top > 1;
+    const bool few = b0 == -INFINITY || (two && b1 == -INFINITY);
+    const double s = two && b1 != -INFINITY ? b0 + b1 : b0;
+    gkeys[g] = nan && few ? 1 : order_key(s, b0 == -INFINITY);
+  }
+  __syncwarp();
+  // keys in place of the scores, 0 outside the groups that stay
+  for (int e = lane; e < a.K; e += 32) {
+    const double x = to_f32(row[e]);
+    uint64_t k = order_key(bias ? cs[e] : x, x == -INFINITY);
+    if (grouped) {
+      const int g = e / a.per;
+      int before = 0;
+      for (int h = 0; h < a.n_groups; ++h)
+        before += gkeys[h] > gkeys[g] || (gkeys[h] == gkeys[g] && h < g);
+      if (before >= a.top_groups) k = 0;
+    }
+    keys[e] = k;
+  }
+  __syncwarp();
+  for (int e = lane; e < a.K; e += 32) {
+    const uint64_t k = keys[e];
+    int before = 0;
+    for (int h = 0; h < a.K; ++h) before += keys[h] > k || (keys[h] == k && h < e);
+    rank[e] = k ? (uint32_t)(a.K - before) : 0;
+  }
+  __syncwarp();
+}
+
+// 32-bit keys in the order of c; equal floats (+0 and -0 too) have equal keys.
+__device__ __forceinline__ uint32_t order_key32(float c, bool dead) {
+  if (dead || c == -INFINITY) return 0;
+  if (c != c) return 1;
+  const int b = __float_as_int(c + 0.f);
+  return b < 0 ? ~(uint32_t)b : (uint32_t)b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// How far apart two f32 selection scores of at most this size have to be for
+// their order to hold in 64 bits: s is off by less than 8 of its 2^-24 (the
+// argument's rounding times exp's own falling value, exp, sum and division),
+// c by one more rounding, a group's rank by twice that.
+constexpr float ROUTE_NEAR = 1.f / (1 << 20);
+
+// Shared memory per warp, in words of 8 bytes: K + n_groups (64-bit keys; the
+// f32 scores for the groups before that), top_k f32 and i32 of the chosen, K
+// 32-bit ranks.
+__host__ __device__ inline int route_words(int K, int n_groups, int top_k) {
+  return K + n_groups + top_k + (K + 1) / 2;
+}
+
+template <int NPL, bool BY_SCORE, typename T>  // NPL experts a lane: e = lane + 32 i
+__global__ void __launch_bounds__(32 * ROUTE_WARPS)
+    k_route(RouteArgs a, int64_t n, const T *__restrict__ logits, const float *__restrict__ bias,
+            float *__restrict__ weights, int *__restrict__ index, int *__restrict__ counts) {
   extern __shared__ uint64_t sm[];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  uint64_t *keys = sm + (size_t)w * (a.K + a.n_groups + a.top_k), *gkeys = keys + a.K;
-  double *cs = reinterpret_cast<double *>(keys);
-  float *picked = reinterpret_cast<float *>(gkeys + a.n_groups);
-  for (int64_t t = blockIdx.x * (int64_t)ROUTE_WARPS + w; t < n;
-       t += (int64_t)gridDim.x * ROUTE_WARPS) {
-    float x[NPL];
-    float m = -INFINITY;
+  uint64_t *keys = sm + (size_t)w * route_words(a.K, a.n_groups, a.top_k);
+  float *cs = reinterpret_cast<float *>(keys);
+  float *picked = reinterpret_cast<float *>(keys + a.K + a.n_groups);
+  int *chosen = reinterpret_cast<int *>(picked + a.top_k);
+  uint32_t *rank = reinterpret_cast<uint32_t *>(chosen + a.top_k);
+  int *hist = reinterpret_cast<int *>(sm + (size_t)ROUTE_WARPS * route_words(a.K, a.n_groups, a.top_k));
+  if (counts) {
+    for (int e = threadIdx.x; e < a.K; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+  }
+  const int64_t step = (int64_t)gridDim.x * ROUTE_WARPS;
+  int64_t t = blockIdx.x * (int64_t)ROUTE_WARPS + w;
+  float xn[NPL];
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int e = lane + 32 * i;
-      x[i] = e < a.K ? to_f32(logits[t * a.K + e]) : -INFINITY;
-      m = fmaxf(m, x[i]);
+  for (int i = 0; i < NPL; ++i)
+    xn[i] = t < n && lane + 32 * i < a.K ? to_f32(logits[t * a.K + lane + 32 * i]) : -INFINITY;
+  float b[NPL];
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) b[i] = BY_SCORE && bias && lane + 32 * i < a.K ? bias[lane + 32 * i] : 0.f;
+  for (; t < n; t += step) {
+    float x[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) x[i] = xn[i];
+    if (t + step < n) {  // the next row's logits, under this row's work
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (lane + 32 * i < a.K) xn[i] = to_f32(logits[(t + step) * a.K + lane + 32 * i]);
     }
-    m = warp_max(m);
-    const float m0 = m == -INFINITY ? 0.f : m;  // a row without any expert
-    float z = 0.f;
-    if (a.softmax) {
+    float m0 = 0.f, z = 1.f;
+    if (a.softmax && (BY_SCORE || !a.renorm)) {
+      m0 = x[0];
+#pragma unroll
+      for (int i = 1; i < NPL; ++i) m0 = fmaxf(m0, x[i]);
+      m0 = warp_max(m0);
+      if (m0 == -INFINITY) m0 = 0.f;  // a row without any expert
+      z = 0.f;
 #pragma unroll
       for (int i = 0; i < NPL; ++i) z += expf(x[i] - m0);
       z = warp_sum(z);
     }
-    // selection keys
-    const bool by_score = bias != nullptr || (a.top_groups < a.n_groups && a.group_top > 1);
-    double z64 = 0.0;
-    if (by_score && a.softmax) {
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) z64 += exp((double)x[i] - m0);
-      z64 = warp_sum(z64);
-    }
-    uint64_t key[NPL];
+    uint32_t key[NPL];
+    float size = 0.f;  // BY_SCORE: the scores' largest magnitude, for what counts as near
+    bool again = false;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       const int e = lane + 32 * i;
-      const bool dead = x[i] == -INFINITY;
-      double c = x[i];
-      if (by_score) {
-        c = a.softmax ? exp((double)x[i] - m0) / z64 : 1.0 / (1.0 + exp(-(double)x[i]));
-        if (bias && e < a.K) c += bias[e];
+      const bool dead = x[i] == -INFINITY || e >= a.K;
+      float c = x[i];
+      if (BY_SCORE) {
+        const float s = a.softmax ? expf(x[i] - m0) / z : sigmoid_f(x[i]);
+        c = s + b[i];
+        again |= !dead && c != c;  // NaN: let 64 bits sort it out
+        if (!dead && c != -INFINITY) size = fmaxf(size, fmaxf(s, fabsf(c)));
       }
-      key[i] = e < a.K ? order_key(bias ? c : (double)x[i], dead) : 0;
-      if (e < a.K && a.top_groups < a.n_groups) cs[e] = dead ? -INFINITY : c;
+      key[i] = order_key32(bias || !BY_SCORE ? c : x[i], dead);
+      if (a.top_groups < a.n_groups && e < a.K) cs[e] = dead ? -INFINITY : c;
     }
+    float tol = 0.f;
+    if (BY_SCORE) tol = warp_max(size) * ROUTE_NEAR;
     if (a.top_groups < a.n_groups) {
       __syncwarp();
+      // lane g ranks group g (more than 32 groups: lane g ranks g, g + 32, ...)
+      uint32_t *gk = reinterpret_cast<uint32_t *>(cs + a.K);
       for (int g = lane; g < a.n_groups; g += 32) {
-        double b0 = -INFINITY, b1 = -INFINITY;  // NaN ranks below every number
+        float b0 = -INFINITY, b1 = -INFINITY;
         bool nan = false;
         for (int j = 0; j < a.per; ++j) {
-          const double c = cs[g * a.per + j];
-          if (c != c) { nan = true; continue; }
-          if (c > b0) b1 = b0, b0 = c;
-          else if (c > b1) b1 = c;
+          const float c = cs[g * a.per + j];
+          nan |= c != c;
+          b1 = fmaxf(b1, fminf(b0, c));
+          b0 = fmaxf(b0, c);
         }
-        // a NaN counts where too few numbers are left
-        const bool use2 = a.group_top > 1;
-        double s = b0;
-        if (use2 && b1 != -INFINITY) s += b1;
-        const bool short_ = b0 == -INFINITY || (use2 && b1 == -INFINITY);
-        gkeys[g] = nan && short_ ? 1 : order_key(s, b0 == -INFINITY);
+        // (fmaxf and fminf leave a NaN out; b1 after one is set right in 64 bits)
+        uint32_t k = order_key32(a.group_top > 1 && b1 != -INFINITY ? b0 + b1 : b0, b0 == -INFINITY);
+        if (nan && b0 == -INFINITY) k = 1;
+        gk[g] = k;
       }
       __syncwarp();
-      // group g stays if fewer than top_groups groups come before it
-      uint64_t keep = 0;  // of this lane's experts
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const int e = lane + 32 * i;
-        if (e >= a.K) continue;
-        const int g = e / a.per;
-        const uint64_t k = gkeys[g];
+      uint32_t floor_key = 0xffffffffu, next_key = 0;  // the last group that stays, the first that does not
+      for (int g = lane; g < a.n_groups; g += 32) {
+        const uint32_t k = gk[g];
         int before = 0;
-        for (int h = 0; h < a.n_groups; ++h)
-          before += gkeys[h] > k || (gkeys[h] == k && h < g);
-        if (before < a.top_groups) keep |= 1ull << i;
+        for (int h = 0; h < a.n_groups; ++h) before += gk[h] > k || (gk[h] == k && h < g);
+        if (before == a.top_groups - 1) floor_key = k;
+        if (before == a.top_groups) next_key = k;
+        cs[g] = before < a.top_groups ? 1.f : 0.f;  // (the scores are not read any more)
+      }
+      __syncwarp();
+      if (BY_SCORE) {
+        floor_key = __reduce_min_sync(0xffffffffu, floor_key);
+        next_key = __reduce_max_sync(0xffffffffu, next_key);
+        if (next_key > 1)
+          again |= !(key_value(floor_key) - key_value(next_key) > 2.f * tol);
       }
 #pragma unroll
       for (int i = 0; i < NPL; ++i)
-        if (!((keep >> i) & 1)) key[i] = 0;
+        if (lane + 32 * i < a.K && cs[(lane + 32 * i) / a.per] == 0.f) key[i] = 0;
       __syncwarp();
     }
-    // weights of all experts, or the top_k rounds of selection
-    float total = 0.f;
-    if (a.top_k == a.K) {
-      float mc = -INFINITY;
+    if (BY_SCORE && __any_sync(0xffffffffu, again)) {
+      rank_in_64_bits(a, logits + t * a.K, m0, bias, keys, rank);
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) key[i] = lane + 32 * i < a.K ? rank[lane + 32 * i] : 0;
+      tol = -1.f;  // ranks: nothing is near
+    }
+    if (a.top_k == a.K) {  // nothing to select: slot e is expert e
+      float mc = -INFINITY, total = 0.f;
 #pragma unroll
       for (int i = 0; i < NPL; ++i)
         if (key[i]) mc = fmaxf(mc, x[i]);
@@ -152,12 +258,10 @@ __global__ void k_route(RouteArgs a, int64_t n, const T *__restrict__ logits,
       for (int i = 0; i < NPL; ++i) {
         s[i] = 0.f;
         if (key[i])
-          s[i] = !a.softmax ? sigmoid_f(x[i])
-                 : a.renorm ? expf(x[i] - mc)
-                            : expf(x[i] - m0) / z;
+          s[i] = !a.softmax ? sigmoid_f(x[i]) : a.renorm ? expf(x[i] - mc) : expf(x[i] - m0) / z;
         total += s[i];
       }
-      total = warp_sum(total);
+      if (a.renorm) total = warp_sum(total);
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
         const int e = lane + 32 * i;
@@ -166,129 +270,212 @@ __global__ void k_route(RouteArgs a, int64_t n, const T *__restrict__ logits,
         if (a.renorm) v = total == 0.f ? 0.f : v / total;
         weights[t * a.K + e] = key[i] ? v * a.scale : 0.f;
         index[t * a.K + e] = key[i] ? e : -1;
-        if (counts && key[i]) atomicAdd(&counts[e], 1);
+        if (counts && key[i]) atomicAdd(&hist[e], 1);
       }
       continue;
     }
-    float mc = 0.f;
-    for (int j = 0; j < a.top_k; ++j) {
-      uint64_t bk = 0;
-      int be = 0x7fffffff;
+    // top_k rounds: the largest key, then the lowest index that has it
+    for (;;) {
+      uint32_t live[NPL];
 #pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (key[i] > bk) bk = key[i], be = lane + 32 * i;
-      warp_best(bk, be);
-      const bool live = bk != 0;
-      float xv = 0.f;
+      for (int i = 0; i < NPL; ++i) live[i] = key[i];
+      uint32_t prev = 0;
+      float prev_x = 0.f, prev_b = 0.f;
+      bool near = false;
+      for (int j = 0; j < a.top_k; ++j) {
+        uint32_t lk = live[0];
+        int li = 0;
 #pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (live && be == lane + 32 * i) xv = x[i], key[i] = 0;
-      if (live) xv = __shfl_sync(0xffffffffu, xv, be & 31);
-      if (lane == 0) {
-        picked[j] = xv;
-        index[t * a.top_k + j] = live ? be : -1;
-        if (counts && live) atomicAdd(&counts[be], 1);
+        for (int i = 1; i < NPL; ++i)
+          if (live[i] > lk) lk = live[i], li = i;
+        const uint32_t bk = __reduce_max_sync(0xffffffffu, lk);
+        const uint32_t be =
+            __reduce_min_sync(0xffffffffu, lk == bk ? (uint32_t)(lane + 32 * li) : 0xffffffffu);
+        const bool mine = bk != 0 && (be & 31) == lane;
+        float xv = 0.f, bv = 0.f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+          if (mine && (int)(be >> 5) == i) xv = x[i], bv = b[i], live[i] = 0;
+        if (BY_SCORE && tol >= 0.f) {
+          xv = __shfl_sync(0xffffffffu, xv, be & 31);
+          bv = __shfl_sync(0xffffffffu, bv, be & 31);
+          // scores this close may stand the other way round in 64 bits, unless
+          // they come from the same numbers
+          if (j > 0 && bk > 1 && bias && !(key_value(prev) - key_value(bk) > tol) &&
+              !(xv == prev_x && bv == prev_b))
+            near = true;
+          prev = bk, prev_x = xv, prev_b = bv;
+          if (lane == 0) picked[j] = xv, chosen[j] = bk ? (int)be : -1;
+        } else {
+          if (mine) picked[j] = xv, chosen[j] = (int)be;
+          if (bk == 0 && lane == 0) chosen[j] = -1;
+        }
       }
-      if (live) mc = j == 0 ? xv : fmaxf(mc, xv);
+      if (BY_SCORE && tol >= 0.f && bias && prev > 1) {
+        // the last one chosen and those left over
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+          near |= live[i] > 1 && !(key_value(prev) - key_value(live[i]) > tol) &&
+                  !(x[i] == prev_x && b[i] == prev_b);
+        near = __any_sync(0xffffffffu, near);
+      }
+      if (!near) break;
+      rank_in_64_bits(a, logits + t * a.K, m0, bias, keys, rank);
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) key[i] = lane + 32 * i < a.K ? rank[lane + 32 * i] : 0;
+      tol = -1.f;
     }
     __syncwarp();
-    for (int pass = 0; pass < 2; ++pass) {
-      // pass 0: the sum of the chosen scores; pass 1: the weights
-      for (int j = lane; j < a.top_k; j += 32) {
-        const bool live = index[t * a.top_k + j] >= 0;
-        float s = 0.f;
-        if (live)
-          s = !a.softmax ? sigmoid_f(picked[j])
-              : a.renorm ? expf(picked[j] - mc)
-                         : expf(picked[j] - m0) / z;
-        if (pass == 0)
-          total += s;
-        else
-          weights[t * a.top_k + j] =
-              !live ? 0.f : (a.renorm ? (total == 0.f ? 0.f : s / total) : s) * a.scale;
+    float mc = -INFINITY, total = 0.f;
+    if (a.softmax && a.renorm) {
+      for (int j = lane; j < a.top_k; j += 32)
+        if (chosen[j] >= 0) mc = fmaxf(mc, picked[j]);
+      mc = warp_max(mc);
+    }
+    auto score = [&](float v) {
+      return !a.softmax ? sigmoid_f(v) : a.renorm ? expf(v - mc) : expf(v - m0) / z;
+    };
+    if (a.renorm) {
+      for (int j = lane; j < a.top_k; j += 32)
+        if (chosen[j] >= 0) total += score(picked[j]);
+      total = warp_sum(total);
+    }
+    for (int j = lane; j < a.top_k; j += 32) {
+      const int e = chosen[j];
+      float v = 0.f;
+      if (e >= 0) {
+        v = score(picked[j]);
+        if (a.renorm) v = total == 0.f ? 0.f : v / total;
+        v *= a.scale;
+        if (counts) atomicAdd(&hist[e], 1);
       }
-      if (pass == 0) total = warp_sum(total);
+      weights[t * a.top_k + j] = v;
+      index[t * a.top_k + j] = e;
     }
     __syncwarp();
   }
+  if (counts) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.K; e += blockDim.x) {
+      if (gridDim.x == 1) counts[e] = hist[e];
+      else if (hist[e]) atomicAdd(&counts[e], hist[e]);
+    }
+  }
 }
 
-// Shared memory per warp: gs [K] f32, chosen flags in its own array.
-template <int NPL, typename T>
-__global__ void k_route_grad(RouteArgs a, int64_t n, const T *__restrict__ logits,
-                             const int *__restrict__ index, const float *__restrict__ gw,
-                             float *__restrict__ grad) {
+// FULL: softmax without renormalisation, whose gradient reaches every logit;
+// otherwise it reaches the chosen ones alone and the others are not read.
+// Shared memory per warp: the row's gradient [K].
+template <int NPL, bool FULL, typename T>
+__global__ void __launch_bounds__(32 * ROUTE_WARPS)
+    k_route_grad(RouteArgs a, int64_t n, const T *__restrict__ logits, const int *__restrict__ index,
+                 const float *__restrict__ gw, float *__restrict__ grad) {
   extern __shared__ float gsm[];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   float *gs = gsm + (size_t)w * a.K;
   for (int64_t t = blockIdx.x * (int64_t)ROUTE_WARPS + w; t < n;
        t += (int64_t)gridDim.x * ROUTE_WARPS) {
+    const T *row = logits + t * a.K;
+    // this lane's first slot; slots beyond 32 are read again below
+    int e0 = -1;
+    float v0 = 0.f, g0 = 0.f;
+    auto slot = [&](int j, int &e, float &v, float &g) {
+      e = j < a.top_k ? index[t * a.top_k + j] : -1;
+      if (e < 0 || e >= a.K) e = -1;
+      v = e >= 0 ? to_f32(row[e]) : 0.f;
+      g = e >= 0 ? gw[t * a.top_k + j] : 0.f;
+    };
+    slot(lane, e0, v0, g0);
     float x[NPL];
-    float m = -INFINITY;
+    float m0 = 0.f, z = 1.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       const int e = lane + 32 * i;
-      x[i] = e < a.K ? to_f32(logits[t * a.K + e]) : -INFINITY;
-      m = fmaxf(m, x[i]);
+      if (FULL) x[i] = e < a.K ? to_f32(row[e]) : -INFINITY;
       if (e < a.K) gs[e] = 0.f;
     }
-    m = warp_max(m);
-    const float m0 = m == -INFINITY ? 0.f : m;
-    float z = 1.f;
-    if (a.softmax && !a.renorm) {
+    if (FULL) {
+      m0 = x[0];
+#pragma unroll
+      for (int i = 1; i < NPL; ++i) m0 = fmaxf(m0, x[i]);
+      m0 = warp_max(m0);
+      if (m0 == -INFINITY) m0 = 0.f;
       z = 0.f;
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) z += expf(x[i] - m0);
+      for (int i = 0; i < NPL; ++i) {
+        x[i] = expf(x[i] - m0);
+        z += x[i];
+      }
       z = warp_sum(z);
     }
-    // the chosen logits' largest, the sum of the chosen scores
-    float mc = -INFINITY, total = 0.f, dot = 0.f;
+    float mc = 0.f, total = 1.f, dot = 0.f;
     if (a.renorm) {
-      for (int j = lane; j < a.top_k; j += 32) {
-        const int e = index[t * a.top_k + j];
-        if (e >= 0 && e < a.K) mc = fmaxf(mc, to_f32(logits[t * a.K + e]));
-      }
-      mc = warp_max(mc);
-      if (mc == -INFINITY) mc = 0.f;  // no slot in use
-      for (int j = lane; j < a.top_k; j += 32) {
-        const int e = index[t * a.top_k + j];
-        if (e >= 0 && e < a.K) {
-          const float v = to_f32(logits[t * a.K + e]);
-          total += a.softmax ? expf(v - mc) : sigmoid_f(v);
+      // the chosen scores over their sum, and its product with the gradient
+      if (a.softmax) {
+        mc = e0 >= 0 ? v0 : -INFINITY;
+        for (int j = lane + 32; j < a.top_k; j += 32) {
+          int e;
+          float v, g;
+          slot(j, e, v, g);
+          if (e >= 0) mc = fmaxf(mc, v);
         }
+        mc = warp_max(mc);
+        if (mc == -INFINITY) mc = 0.f;  // no slot in use
+      }
+      const float s0 = e0 < 0 ? 0.f : a.softmax ? expf(v0 - mc) : sigmoid_f(v0);
+      total = s0;
+      for (int j = lane + 32; j < a.top_k; j += 32) {
+        int e;
+        float v, g;
+        slot(j, e, v, g);
+        if (e >= 0) total += a.softmax ? expf(v - mc) : sigmoid_f(v);
       }
       total = warp_sum(total);
-      for (int j = lane; j < a.top_k; j += 32) {
-        const int e = index[t * a.top_k + j];
-        if (e >= 0 && e < a.K && total != 0.f) {
-          const float v = to_f32(logits[t * a.K + e]);
-          dot += gw[t * a.top_k + j] * ((a.softmax ? expf(v - mc) : sigmoid_f(v)) / total);
+      if (total != 0.f) {
+        dot = e0 < 0 ? 0.f : g0 * (s0 / total);
+        for (int j = lane + 32; j < a.top_k; j += 32) {
+          int e;
+          float v, g;
+          slot(j, e, v, g);
+          if (e >= 0) dot += g * ((a.softmax ? expf(v - mc) : sigmoid_f(v)) / total);
         }
       }
       dot = warp_sum(dot);
     }
     __syncwarp();
-    // gradients of the scores (an expert named twice adds up, in slot order)
-    if (lane == 0)
-      for (int j = 0; j < a.top_k; ++j) {
-        const int e = index[t * a.top_k + j];
-        if (e < 0 || e >= a.K || (a.renorm && total == 0.f)) continue;
-        const float v = to_f32(logits[t * a.K + e]);
-        const float g = (gw[t * a.top_k + j] - dot) * a.scale;
-        float d;  // score times (for softmax) or derivative times the gradient
-        if (a.softmax)
-          d = a.renorm ? expf(v - mc) / total * g : g;
-        else
-          d = (a.renorm ? g / total : g) * sigmoid_f(v) * sigmoid_f(-v);
+    // Gradients of the scores (sigmoid, renormalised: of the logits), 32 slots
+    // at a time; an expert named twice in them adds up in slot order.
+    for (int j = 0; j < a.top_k; j += 32) {
+      int e = e0;
+      float v = v0, g = g0;
+      if (j > 0) slot(j + lane, e, v, g);
+      float d = 0.f;
+      if (e >= 0 && !(a.renorm && total == 0.f)) {
+        d = (g - dot) * a.scale;
+        if (a.softmax) {
+          if (a.renorm) d *= expf(v - mc) / total;
+        } else {
+          d = (a.renorm ? d / total : d) * sigmoid_f(v) * sigmoid_f(-v);
+        }
+      }
+      const unsigned same = __match_any_sync(0xffffffffu, e);
+      const bool twice = e >= 0 && __popc(same) > 1;
+      if (__any_sync(0xffffffffu, twice)) {
+        for (int l = 0; l < 32; ++l) {
+          if (lane == l && e >= 0) gs[e] += d;
+          __syncwarp();
+        }
+      } else if (e >= 0) {
         gs[e] += d;
       }
-    __syncwarp();
+      __syncwarp();
+    }
     float sdot = 0.f;
-    if (a.softmax && !a.renorm) {
+    if (FULL) {
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
         const int e = lane + 32 * i;
-        if (e < a.K && gs[e] != 0.f) sdot += expf(x[i] - m0) / z * gs[e];
+        if (e < a.K && gs[e] != 0.f) sdot += x[i] / z * gs[e];
       }
       sdot = warp_sum(sdot);
     }
@@ -297,7 +484,7 @@ __global__ void k_route_grad(RouteArgs a, int64_t n, const T *__restrict__ logit
       const int e = lane + 32 * i;
       if (e >= a.K) continue;
       float g = gs[e];
-      if (a.softmax && !a.renorm) g = z == 0.f ? 0.f : expf(x[i] - m0) / z * (g - sdot);
+      if (FULL) g = z == 0.f ? 0.f : x[i] / z * (g - sdot);
       grad[t * a.K + e] = g;
     }
     __syncwarp();
@@ -360,26 +547,48 @@ int route_grid(int64_t n) {
   return (int)(want < MODEL_SMS * 16 ? want : MODEL_SMS * 16);
 }
 
-template <int NPL, typename T>
-so2_status run_route(const RouteArgs &a, int64_t n, const void *logits, const float *bias,
+template <int NPL, bool BY_SCORE, typename T>
+so2_status run_route(const RouteArgs &a, int64_t n, const T *logits, const float *bias,
                      float *weights, int32_t *index, int32_t *counts, cudaStream_t s) {
-  const int smem = ROUTE_WARPS * (a.K + a.n_groups + a.top_k) * 8;
+  const int smem = ROUTE_WARPS * route_words(a.K, a.n_groups, a.top_k) * 8 + a.K * 4;
   if (smem > 48 * 1024)
-    MODEL_CK(cudaFuncSetAttribute(k_route<NPL, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  k_route<NPL, T><<<route_grid(n), 32 * ROUTE_WARPS, smem, s>>>(
-      a, n, static_cast<const T *>(logits), bias, weights, index, counts);
+    MODEL_CK(cudaFuncSetAttribute(k_route<NPL, BY_SCORE, T>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  // up to 16 rows one block stores the counts itself, without a clearing launch
+  const int grid = n <= 16 ? 1 : route_grid(n);
+  if (counts && grid > 1) MODEL_CK(cudaMemsetAsync(counts, 0, sizeof(int32_t) * a.K, s));
+  k_route<NPL, BY_SCORE, T><<<grid, 32 * ROUTE_WARPS, smem, s>>>(a, n, logits, bias, weights, index,
+                                                                 counts);
   MODEL_CKL();
   return SO2_OK;
 }
 
+template <typename T>
+so2_status run_route(const RouteArgs &a, int64_t n, const void *logits, const float *bias,
+                     float *weights, int32_t *index, int32_t *counts, cudaStream_t s) {
+  const T *x = static_cast<const T *>(logits);
+  if (bias || (a.top_groups < a.n_groups && a.group_top > 1))
+    ROUTE_DISPATCH(a.K, return run_route<NPL, true, T>(a, n, x, bias, weights, index, counts, s))
+  ROUTE_DISPATCH(a.K, return run_route<NPL, false, T>(a, n, x, bias, weights, index, counts, s))
+}
+
 template <int NPL, typename T>
-so2_status run_route_grad(const RouteArgs &a, int64_t n, const void *logits, const int32_t *index,
+so2_status run_route_grad(const RouteArgs &a, int64_t n, const T *logits, const int32_t *index,
                           const float *gw, float *grad, cudaStream_t s) {
-  const int smem = ROUTE_WARPS * a.K * 4;
-  k_route_grad<NPL, T><<<route_grid(n), 32 * ROUTE_WARPS, smem, s>>>(
-      a, n, static_cast<const T *>(logits), index, gw, grad);
+  const int smem = ROUTE_WARPS * a.K * 4, threads = 32 * ROUTE_WARPS;
+  if (a.softmax && !a.renorm)
+    k_route_grad<NPL, true, T><<<route_grid(n), threads, smem, s>>>(a, n, logits, index, gw, grad);
+  else
+    k_route_grad<NPL, false, T><<<route_grid(n), threads, smem, s>>>(a, n, logits, index, gw, grad);
   MODEL_CKL();
   return SO2_OK;
+}
+
+template <typename T>
+so2_status run_route_grad(const RouteArgs &a, int64_t n, const void *logits, const int32_t *index,
+                          const float *gw, float *grad, cudaStream_t s) {
+  const T *x = static_cast<const T *>(logits);
+  ROUTE_DISPATCH(a.K, return run_route_grad<NPL, T>(a, n, x, index, gw, grad, s))
 }
 
 }  // namespace
@@ -396,12 +605,13 @@ so2_status so2conv_route_forward(const so2conv_route_desc *d, int64_t n, const v
       !aligned_to(counts, 4))
     return SO2_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (counts) MODEL_CK(cudaMemsetAsync(counts, 0, sizeof(int32_t) * d->n_experts, s));
-  if (n == 0) return SO2_OK;
+  if (n == 0) {
+    if (counts) MODEL_CK(cudaMemsetAsync(counts, 0, sizeof(int32_t) * d->n_experts, s));
+    return SO2_OK;
+  }
   const RouteArgs a = route_args(d);
-  if (d->dtype == SO2_F32)
-    ROUTE_DISPATCH(a.K, return run_route<NPL, float>(a, n, logits, bias, weights, index, counts, s))
-  ROUTE_DISPATCH(a.K, return run_route<NPL, __nv_bfloat16>(a, n, logits, bias, weights, index, counts, s))
+  if (d->dtype == SO2_F32) return run_route<float>(a, n, logits, bias, weights, index, counts, s);
+  return run_route<__nv_bfloat16>(a, n, logits, bias, weights, index, counts, s);
 }
 
 so2_status so2conv_route_backward(const so2conv_route_desc *d, int64_t n, const void *logits,
@@ -414,9 +624,8 @@ so2_status so2conv_route_backward(const so2conv_route_desc *d, int64_t n, const 
   if (n == 0) return SO2_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const RouteArgs a = route_args(d);
-  if (d->dtype == SO2_F32)
-    ROUTE_DISPATCH(a.K, return run_route_grad<NPL, float>(a, n, logits, index, gw, grad, s))
-  ROUTE_DISPATCH(a.K, return run_route_grad<NPL, __nv_bfloat16>(a, n, logits, index, gw, grad, s))
+  if (d->dtype == SO2_F32) return run_route_grad<float>(a, n, logits, index, gw, grad, s);
+  return run_route_grad<__nv_bfloat16>(a, n, logits, index, gw, grad, s);
 }
 
 }  // extern "C"
