@@ -113,11 +113,10 @@ __device__ __noinline__ void rank_in_64_bits(const RouteArgs &a, const T *__rest
 }
 
 // 32-bit keys in the order of c; equal floats (+0 and -0 too) have equal keys.
-__device__ __forceinline__ uint32_t order_key32(float c, bool dead) {
-  if (dead || c == -INFINITY) return 0;
-  if (c != c) return 1;
+__device__ __forceinline__ uint32_t order_key32(float c, bool dead = false) {
   const int b = __float_as_int(c + 0.f);
-  return b < 0 ? ~(uint32_t)b : (uint32_t)b | 0x80000000u;
+  const uint32_t k = (uint32_t)b ^ ((uint32_t)(b >> 31) | 0x80000000u);
+  return dead || c == -INFINITY ? 0u : c != c ? 1u : k;
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
@@ -129,47 +128,85 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // c by one more rounding, a group's rank by twice that.
 constexpr float ROUTE_NEAR = 1.f / (1 << 20);
 
-// Shared memory per warp, in words of 8 bytes: K + n_groups (64-bit keys; the
-// f32 scores for the groups before that), top_k f32 and i32 of the chosen, K
-// 32-bit ranks.
-__host__ __device__ inline int route_words(int K, int n_groups, int top_k) {
-  return K + n_groups + top_k + (K + 1) / 2;
+// Shared memory per warp, in words of 8 bytes: the chosen experts (i32); by
+// score also K + n_groups 64-bit keys and K 32-bit ranks, and the groups' f32
+// scores and keys, which come before those, fit there.
+__host__ __device__ inline int route_words(int K, int n_groups, int top_k, bool by_score) {
+  return (top_k + 1) / 2 + (by_score ? K + n_groups + (K + 1) / 2 : n_groups > 1 ? (K + n_groups + 1) / 2 : 0);
 }
 
-template <int NPL, bool BY_SCORE, typename T>  // NPL experts a lane: e = lane + 32 i
+// NPL consecutive experts' values of a row, those of lane `lane`; -inf beyond K.
+template <int NPL, typename T>
+__device__ __forceinline__ void load_experts(const T *__restrict__ row, int K, bool vec,
+                                             float (&x)[NPL]) {
+  const int e0 = (threadIdx.x & 31) * NPL;
+  constexpr int V = NPL * sizeof(T) <= 16 ? NPL : 16 / (int)sizeof(T);
+  if (NPL > 1 && vec) {
+#pragma unroll
+    for (int i = 0; i < NPL; i += V) {
+      if (e0 + i < K) {
+        if constexpr (V == 4 || V == 8) {
+          float r[V];
+          load_vec<V>(row + e0 + i, r);
+#pragma unroll
+          for (int v = 0; v < V; ++v) x[i + v] = r[v];
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) x[i + v] = to_f32(row[e0 + i + v]);
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[i + v] = -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) x[i] = e0 + i < K ? to_f32(row[e0 + i]) : -INFINITY;
+  }
+}
+
+// Whether rows of K values can be read in the vectors of load_experts.
+template <int NPL, typename T>
+bool expert_vectors(int K, const T *logits) {
+  constexpr int V = NPL * sizeof(T) <= 16 ? NPL : 16 / (int)sizeof(T);
+  return K % V == 0 && aligned_to(logits, V * sizeof(T));
+}
+
+// NPL experts a lane: e = NPL lane + i, so that of equal keys the lowest lane
+// holds the lowest index.  A round of the selection is one reduction of the
+// lanes' largest keys and one vote for its lane, which notes its expert in
+// shared memory and moves on; up to four keys a lane are sorted beforehand and
+// shifted as they are taken, more are looked through in each round.  The
+// instructions bound this kernel, not memory.
+template <int NPL, bool BY_SCORE, typename T>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS)
-    k_route(RouteArgs a, int64_t n, const T *__restrict__ logits, const float *__restrict__ bias,
-            float *__restrict__ weights, int *__restrict__ index, int *__restrict__ counts) {
+    k_route(RouteArgs a, int64_t n, const T *__restrict__ logits, bool vec,
+            const float *__restrict__ bias, float *__restrict__ weights, int *__restrict__ index,
+            int *__restrict__ counts) {
   extern __shared__ uint64_t sm[];
+  constexpr bool SORTED = NPL <= 4;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  uint64_t *keys = sm + (size_t)w * route_words(a.K, a.n_groups, a.top_k);
+  const int words = route_words(a.K, a.n_groups, a.top_k, BY_SCORE);
+  int *chosen = reinterpret_cast<int *>(sm + w * words);
+  uint64_t *keys = sm + w * words + (a.top_k + 1) / 2;
   float *cs = reinterpret_cast<float *>(keys);
-  float *picked = reinterpret_cast<float *>(keys + a.K + a.n_groups);
-  int *chosen = reinterpret_cast<int *>(picked + a.top_k);
-  uint32_t *rank = reinterpret_cast<uint32_t *>(chosen + a.top_k);
-  int *hist = reinterpret_cast<int *>(sm + (size_t)ROUTE_WARPS * route_words(a.K, a.n_groups, a.top_k));
+  uint32_t *rank = reinterpret_cast<uint32_t *>(keys + a.K + a.n_groups);
+  int *hist = reinterpret_cast<int *>(sm + ROUTE_WARPS * words);
   if (counts) {
     for (int e = threadIdx.x; e < a.K; e += blockDim.x) hist[e] = 0;
     __syncthreads();
   }
+  const bool grouped = a.top_groups < a.n_groups;
   const int64_t step = (int64_t)gridDim.x * ROUTE_WARPS;
   int64_t t = blockIdx.x * (int64_t)ROUTE_WARPS + w;
-  float xn[NPL];
-#pragma unroll
-  for (int i = 0; i < NPL; ++i)
-    xn[i] = t < n && lane + 32 * i < a.K ? to_f32(logits[t * a.K + lane + 32 * i]) : -INFINITY;
-  float b[NPL];
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) b[i] = BY_SCORE && bias && lane + 32 * i < a.K ? bias[lane + 32 * i] : 0.f;
+  float x[NPL], xn[NPL];
+  if (t < n) load_experts<NPL>(logits + t * a.K, a.K, vec, xn);
   for (; t < n; t += step) {
-    float x[NPL];
+    const T *row = logits + t * a.K;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) x[i] = xn[i];
-    if (t + step < n) {  // the next row's logits, under this row's work
-#pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (lane + 32 * i < a.K) xn[i] = to_f32(logits[(t + step) * a.K + lane + 32 * i]);
-    }
+    if (t + step < n)  // the next row's logits, under this row's work
+      load_experts<NPL>(logits + (t + step) * a.K, a.K, vec, xn);
     float m0 = 0.f, z = 1.f;
     if (a.softmax && (BY_SCORE || !a.renorm)) {
       m0 = x[0];
@@ -187,23 +224,22 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
     bool again = false;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      const int e = lane + 32 * i;
-      const bool dead = x[i] == -INFINITY || e >= a.K;
+      const int e = lane * NPL + i;
+      const bool dead = x[i] == -INFINITY;  // beyond K too
       float c = x[i];
       if (BY_SCORE) {
         const float s = a.softmax ? expf(x[i] - m0) / z : sigmoid_f(x[i]);
-        c = s + b[i];
+        c = s + (bias && e < a.K ? bias[e] : 0.f);
         again |= !dead && c != c;  // NaN: let 64 bits sort it out
         if (!dead && c != -INFINITY) size = fmaxf(size, fmaxf(s, fabsf(c)));
       }
       key[i] = order_key32(bias || !BY_SCORE ? c : x[i], dead);
-      if (a.top_groups < a.n_groups && e < a.K) cs[e] = dead ? -INFINITY : c;
+      if (grouped && e < a.K) cs[e] = dead ? -INFINITY : c;
     }
     float tol = 0.f;
     if (BY_SCORE) tol = warp_max(size) * ROUTE_NEAR;
-    if (a.top_groups < a.n_groups) {
+    if (grouped) {
       __syncwarp();
-      // lane g ranks group g (more than 32 groups: lane g ranks g, g + 32, ...)
       uint32_t *gk = reinterpret_cast<uint32_t *>(cs + a.K);
       for (int g = lane; g < a.n_groups; g += 32) {
         float b0 = -INFINITY, b1 = -INFINITY;
@@ -214,7 +250,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
           b1 = fmaxf(b1, fminf(b0, c));
           b0 = fmaxf(b0, c);
         }
-        // (fmaxf and fminf leave a NaN out; b1 after one is set right in 64 bits)
+        // (fmaxf and fminf leave a NaN out; by score, 64 bits look at the row)
         uint32_t k = order_key32(a.group_top > 1 && b1 != -INFINITY ? b0 + b1 : b0, b0 == -INFINITY);
         if (nan && b0 == -INFINITY) k = 1;
         gk[g] = k;
@@ -233,21 +269,23 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
       if (BY_SCORE) {
         floor_key = __reduce_min_sync(0xffffffffu, floor_key);
         next_key = __reduce_max_sync(0xffffffffu, next_key);
-        if (next_key > 1)
-          again |= !(key_value(floor_key) - key_value(next_key) > 2.f * tol);
+        if (next_key > 1) again |= !(key_value(floor_key) - key_value(next_key) > 2.f * tol);
       }
 #pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (lane + 32 * i < a.K && cs[(lane + 32 * i) / a.per] == 0.f) key[i] = 0;
+      for (int i = 0; i < NPL; ++i) {
+        const int e = lane * NPL + i;
+        if (e < a.K && cs[e / a.per] == 0.f) key[i] = 0;
+      }
       __syncwarp();
     }
-    if (BY_SCORE && __any_sync(0xffffffffu, again)) {
-      rank_in_64_bits(a, logits + t * a.K, m0, bias, keys, rank);
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) key[i] = lane + 32 * i < a.K ? rank[lane + 32 * i] : 0;
-      tol = -1.f;  // ranks: nothing is near
-    }
+    again = BY_SCORE && __any_sync(0xffffffffu, again);
+
     if (a.top_k == a.K) {  // nothing to select: slot e is expert e
+      if (again) {  // (only to know which experts may not be chosen)
+        rank_in_64_bits(a, row, m0, bias, keys, rank);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) key[i] = lane * NPL + i < a.K ? rank[lane * NPL + i] : 0;
+      }
       float mc = -INFINITY, total = 0.f;
 #pragma unroll
       for (int i = 0; i < NPL; ++i)
@@ -264,7 +302,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
       if (a.renorm) total = warp_sum(total);
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
-        const int e = lane + 32 * i;
+        const int e = lane * NPL + i;
         if (e >= a.K) continue;
         float v = s[i];
         if (a.renorm) v = total == 0.f ? 0.f : v / total;
@@ -274,82 +312,117 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
       }
       continue;
     }
-    // top_k rounds: the largest key, then the lowest index that has it
+
     for (;;) {
-      uint32_t live[NPL];
+      if (again) {
+        rank_in_64_bits(a, row, m0, bias, keys, rank);
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) live[i] = key[i];
+        for (int i = 0; i < NPL; ++i) key[i] = lane * NPL + i < a.K ? rank[lane * NPL + i] : 0;
+      }
+      const bool look = BY_SCORE && !again && bias;
+      uint32_t k[NPL];
+      int id[NPL];
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) k[i] = key[i], id[i] = lane * NPL + i;
+      if constexpr (SORTED) {  // falling, equal keys by index: insertion
+#pragma unroll
+        for (int p = 1; p < NPL; ++p)
+#pragma unroll
+          for (int q = p; q > 0; --q) {
+            const bool swap = k[q] > k[q - 1];
+            const uint32_t kt = k[q];
+            const int it = id[q];
+            k[q] = swap ? k[q - 1] : kt, id[q] = swap ? id[q - 1] : it;
+            k[q - 1] = swap ? kt : k[q - 1], id[q - 1] = swap ? it : id[q - 1];
+          }
+      }
       uint32_t prev = 0;
-      float prev_x = 0.f, prev_b = 0.f;
+      int j = 0;
       bool near = false;
-      for (int j = 0; j < a.top_k; ++j) {
-        uint32_t lk = live[0];
-        int li = 0;
+      for (; j < a.top_k; ++j) {
+        uint32_t lk = k[0];
+        int li = id[0];
+        if constexpr (!SORTED) {
 #pragma unroll
-        for (int i = 1; i < NPL; ++i)
-          if (live[i] > lk) lk = live[i], li = i;
+          for (int i = 1; i < NPL; ++i)
+            if (k[i] > lk) lk = k[i], li = id[i];
+        }
         const uint32_t bk = __reduce_max_sync(0xffffffffu, lk);
-        const uint32_t be =
-            __reduce_min_sync(0xffffffffu, lk == bk ? (uint32_t)(lane + 32 * li) : 0xffffffffu);
-        const bool mine = bk != 0 && (be & 31) == lane;
-        float xv = 0.f, bv = 0.f;
+        if (bk == 0) break;  // uniform: nothing is left
+        const int from = __ffs(__ballot_sync(0xffffffffu, lk == bk)) - 1;
+        if (lane == from) {
+          chosen[j] = li;
+          if constexpr (SORTED) {
 #pragma unroll
-        for (int i = 0; i < NPL; ++i)
-          if (mine && (int)(be >> 5) == i) xv = x[i], bv = b[i], live[i] = 0;
-        if (BY_SCORE && tol >= 0.f) {
-          xv = __shfl_sync(0xffffffffu, xv, be & 31);
-          bv = __shfl_sync(0xffffffffu, bv, be & 31);
+            for (int i = 0; i + 1 < NPL; ++i) k[i] = k[i + 1], id[i] = id[i + 1];
+            k[NPL - 1] = 0;
+          } else {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+              if (li == id[i]) k[i] = 0;
+          }
+        }
+        if (BY_SCORE) {
           // scores this close may stand the other way round in 64 bits, unless
           // they come from the same numbers
-          if (j > 0 && bk > 1 && bias && !(key_value(prev) - key_value(bk) > tol) &&
-              !(xv == prev_x && bv == prev_b))
-            near = true;
-          prev = bk, prev_x = xv, prev_b = bv;
-          if (lane == 0) picked[j] = xv, chosen[j] = bk ? (int)be : -1;
-        } else {
-          if (mine) picked[j] = xv, chosen[j] = (int)be;
-          if (bk == 0 && lane == 0) chosen[j] = -1;
+          if (look && j > 0 && !(key_value(prev) - key_value(bk) > tol)) {
+            __syncwarp();
+            const int e = chosen[j], f = chosen[j - 1];
+            near |= !(to_f32(row[e]) == to_f32(row[f]) && bias[e] == bias[f]);
+          }
+          prev = bk;
         }
       }
-      if (BY_SCORE && tol >= 0.f && bias && prev > 1) {
-        // the last one chosen and those left over
+      for (j += lane; j < a.top_k; j += 32) chosen[j] = -1;
+      __syncwarp();
+      if (look && prev != 0) {  // the last one chosen and those left over
+        bool close = false;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i)
-          near |= live[i] > 1 && !(key_value(prev) - key_value(live[i]) > tol) &&
-                  !(x[i] == prev_x && b[i] == prev_b);
-        near = __any_sync(0xffffffffu, near);
+        for (int i = 0; i < NPL; ++i) close |= k[i] != 0 && !(key_value(prev) - key_value(k[i]) > tol);
+        if (__any_sync(0xffffffffu, close)) {
+          const int f = chosen[a.top_k - 1];  // (used: some are left over)
+          const float px = f >= 0 ? to_f32(row[f]) : 0.f, pb = f >= 0 ? bias[f] : 0.f;
+#pragma unroll
+          for (int i = 0; i < NPL; ++i)
+            if (k[i] != 0 && !(key_value(prev) - key_value(k[i]) > tol))
+              near |= !(to_f32(row[id[i]]) == px && bias[id[i]] == pb);
+          near = __any_sync(0xffffffffu, near);
+        }
       }
       if (!near) break;
-      rank_in_64_bits(a, logits + t * a.K, m0, bias, keys, rank);
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) key[i] = lane + 32 * i < a.K ? rank[lane + 32 * i] : 0;
-      tol = -1.f;
+      again = true;
     }
-    __syncwarp();
-    float mc = -INFINITY, total = 0.f;
+    // weights: lane j takes the slots j, j + 32, ...
+    float mc = 0.f, total = 0.f, v0 = 0.f, s0 = 0.f;  // v0, s0: of the first one
+    const int e0 = lane < a.top_k ? chosen[lane] : -1;
+    if (e0 >= 0) v0 = to_f32(row[e0]);
     if (a.softmax && a.renorm) {
-      for (int j = lane; j < a.top_k; j += 32)
-        if (chosen[j] >= 0) mc = fmaxf(mc, picked[j]);
-      mc = warp_max(mc);
+      mc = e0 >= 0 ? v0 : -INFINITY;
+      if (!BY_SCORE) {
+        mc = __shfl_sync(0xffffffffu, mc, 0);  // the largest logit came first
+      } else {
+        for (int j = lane + 32; j < a.top_k; j += 32)
+          if (chosen[j] >= 0) mc = fmaxf(mc, to_f32(row[chosen[j]]));
+        mc = warp_max(mc);
+      }
     }
+    const float iz = a.softmax && !a.renorm ? 1.f / z : 1.f;
     auto score = [&](float v) {
-      return !a.softmax ? sigmoid_f(v) : a.renorm ? expf(v - mc) : expf(v - m0) / z;
+      return !a.softmax ? sigmoid_f(v) : a.renorm ? expf(v - mc) : expf(v - m0) * iz;
     };
+    if (e0 >= 0) s0 = score(v0);
+    float f = a.scale;
     if (a.renorm) {
-      for (int j = lane; j < a.top_k; j += 32)
-        if (chosen[j] >= 0) total += score(picked[j]);
+      total = s0;
+      for (int j = lane + 32; j < a.top_k; j += 32)
+        if (chosen[j] >= 0) total += score(to_f32(row[chosen[j]]));
       total = warp_sum(total);
+      f = total == 0.f ? 0.f : a.scale / total;
     }
     for (int j = lane; j < a.top_k; j += 32) {
-      const int e = chosen[j];
-      float v = 0.f;
-      if (e >= 0) {
-        v = score(picked[j]);
-        if (a.renorm) v = total == 0.f ? 0.f : v / total;
-        v *= a.scale;
-        if (counts) atomicAdd(&hist[e], 1);
-      }
-      weights[t * a.top_k + j] = v;
+      const int e = j == lane ? e0 : chosen[j];
+      if (counts && e >= 0) atomicAdd(&hist[e], 1);
+      weights[t * a.top_k + j] = e < 0 ? 0.f : (j == lane ? s0 : score(to_f32(row[e]))) * f;
       index[t * a.top_k + j] = e;
     }
     __syncwarp();
@@ -365,34 +438,35 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
 
 // FULL: softmax without renormalisation, whose gradient reaches every logit;
 // otherwise it reaches the chosen ones alone and the others are not read.
-// Shared memory per warp: the row's gradient [K].
+// Shared memory per warp: the row's gradient [32 NPL].
 template <int NPL, bool FULL, typename T>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS)
-    k_route_grad(RouteArgs a, int64_t n, const T *__restrict__ logits, const int *__restrict__ index,
-                 const float *__restrict__ gw, float *__restrict__ grad) {
-  extern __shared__ float gsm[];
+    k_route_grad(RouteArgs a, int64_t n, const T *__restrict__ logits, bool vec,
+                 const int *__restrict__ index, const float *__restrict__ gw,
+                 float *__restrict__ grad, bool vec_out) {
+  __shared__ __align__(16) float rows[ROUTE_WARPS][32 * NPL];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  float *gs = gsm + (size_t)w * a.K;
+  float *gs = rows[w];
+  constexpr int V = NPL >= 4 ? 4 : 1;
   for (int64_t t = blockIdx.x * (int64_t)ROUTE_WARPS + w; t < n;
        t += (int64_t)gridDim.x * ROUTE_WARPS) {
     const T *row = logits + t * a.K;
-    // this lane's first slot; slots beyond 32 are read again below
-    int e0 = -1;
-    float v0 = 0.f, g0 = 0.f;
     auto slot = [&](int j, int &e, float &v, float &g) {
       e = j < a.top_k ? index[t * a.top_k + j] : -1;
-      if (e < 0 || e >= a.K) e = -1;
+      g = j < a.top_k ? gw[t * a.top_k + j] : 0.f;
+      if (e < 0 || e >= a.K) e = -1, g = 0.f;
       v = e >= 0 ? to_f32(row[e]) : 0.f;
-      g = e >= 0 ? gw[t * a.top_k + j] : 0.f;
     };
+    int e0;  // this lane's first slot; slots beyond 32 are read again below
+    float v0, g0;
     slot(lane, e0, v0, g0);
     float x[NPL];
     float m0 = 0.f, z = 1.f;
+    if (FULL) load_experts<NPL>(row, a.K, vec, x);
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int e = lane + 32 * i;
-      if (FULL) x[i] = e < a.K ? to_f32(row[e]) : -INFINITY;
-      if (e < a.K) gs[e] = 0.f;
+    for (int i = 0; i < NPL; i += V) {
+      float zero[V] = {};
+      store_vec<V>(gs + i * 32 + lane * V, zero);
     }
     if (FULL) {
       m0 = x[0];
@@ -408,9 +482,10 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
       }
       z = warp_sum(z);
     }
-    float mc = 0.f, total = 1.f, dot = 0.f;
+    // renormalised: the chosen scores over their sum, and its product with the gradient
+    float mc = 0.f, s0 = 0.f, p0 = 0.f, total = 1.f, dot = 0.f;
+    auto score = [&](float v) { return a.softmax ? expf(v - mc) : sigmoid_f(v); };
     if (a.renorm) {
-      // the chosen scores over their sum, and its product with the gradient
       if (a.softmax) {
         mc = e0 >= 0 ? v0 : -INFINITY;
         for (int j = lane + 32; j < a.top_k; j += 32) {
@@ -422,70 +497,89 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
         mc = warp_max(mc);
         if (mc == -INFINITY) mc = 0.f;  // no slot in use
       }
-      const float s0 = e0 < 0 ? 0.f : a.softmax ? expf(v0 - mc) : sigmoid_f(v0);
+      s0 = e0 < 0 ? 0.f : score(v0);
       total = s0;
       for (int j = lane + 32; j < a.top_k; j += 32) {
         int e;
         float v, g;
         slot(j, e, v, g);
-        if (e >= 0) total += a.softmax ? expf(v - mc) : sigmoid_f(v);
+        if (e >= 0) total += score(v);
       }
       total = warp_sum(total);
-      if (total != 0.f) {
-        dot = e0 < 0 ? 0.f : g0 * (s0 / total);
-        for (int j = lane + 32; j < a.top_k; j += 32) {
-          int e;
-          float v, g;
-          slot(j, e, v, g);
-          if (e >= 0) dot += g * ((a.softmax ? expf(v - mc) : sigmoid_f(v)) / total);
-        }
+      if (total == 0.f) total = INFINITY;  // such scores weigh 0
+      p0 = s0 / total;  // (1 for a single slot, whose gradient is then 0)
+      dot = g0 * p0;
+      for (int j = lane + 32; j < a.top_k; j += 32) {
+        int e;
+        float v, g;
+        slot(j, e, v, g);
+        if (e >= 0) dot += g * (score(v) / total);
       }
       dot = warp_sum(dot);
     }
-    __syncwarp();
     // Gradients of the scores (sigmoid, renormalised: of the logits), 32 slots
-    // at a time; an expert named twice in them adds up in slot order.
+    // at a time.  An expert named twice, which its own tag then shows, adds up
+    // in slot order.
     for (int j = 0; j < a.top_k; j += 32) {
       int e = e0;
       float v = v0, g = g0;
       if (j > 0) slot(j + lane, e, v, g);
-      float d = 0.f;
-      if (e >= 0 && !(a.renorm && total == 0.f)) {
-        d = (g - dot) * a.scale;
-        if (a.softmax) {
-          if (a.renorm) d *= expf(v - mc) / total;
-        } else {
-          d = (a.renorm ? d / total : d) * sigmoid_f(v) * sigmoid_f(-v);
-        }
+      float d = (g - dot) * a.scale;
+      if (a.softmax) {
+        if (a.renorm) d *= j == 0 ? p0 : score(v) / total;
+      } else {
+        d *= sigmoid_f(v) * sigmoid_f(-v) / total;
       }
-      const unsigned same = __match_any_sync(0xffffffffu, e);
-      const bool twice = e >= 0 && __popc(same) > 1;
-      if (__any_sync(0xffffffffu, twice)) {
+      __syncwarp();
+      if (j == 0) {
+        if (e >= 0) gs[e] = __int_as_float(lane);
+        __syncwarp();
+        const bool twice = e >= 0 && __float_as_int(gs[e]) != lane;
+        const bool any = __any_sync(0xffffffffu, twice);
+        if (e >= 0) gs[e] = any ? 0.f : d;
+        __syncwarp();
+        if (any)
+          for (int l = 0; l < 32; ++l) {
+            if (lane == l && e >= 0) gs[e] += d;
+            __syncwarp();
+          }
+      } else {
         for (int l = 0; l < 32; ++l) {
           if (lane == l && e >= 0) gs[e] += d;
           __syncwarp();
         }
-      } else if (e >= 0) {
-        gs[e] += d;
       }
-      __syncwarp();
     }
+    __syncwarp();
     float sdot = 0.f;
     if (FULL) {
+      const float iz = z == 0.f ? 0.f : 1.f / z;
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
-        const int e = lane + 32 * i;
-        if (e < a.K && gs[e] != 0.f) sdot += x[i] / z * gs[e];
+        x[i] *= iz;  // the scores
+        const float g = gs[lane * NPL + i];
+        if (g != 0.f) sdot += x[i] * g;
       }
       sdot = warp_sum(sdot);
     }
+    auto value = [&](int i, float g) { return !FULL ? g : z == 0.f ? 0.f : x[i] * (g - sdot); };
+    if (vec_out) {
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int e = lane + 32 * i;
-      if (e >= a.K) continue;
-      float g = gs[e];
-      if (FULL) g = z == 0.f ? 0.f : x[i] / z * (g - sdot);
-      grad[t * a.K + e] = g;
+      for (int i = 0; i < NPL; i += V) {
+        const int e = FULL ? lane * NPL + i : i * 32 + lane * V;
+        if (e >= a.K) continue;
+        float r[V];
+        load_vec<V>(gs + e, r);
+#pragma unroll
+        for (int v = 0; v < V; ++v) r[v] = value(i + v, r[v]);
+        store_vec<V>(grad + t * a.K + e, r);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        const int e = FULL ? lane * NPL + i : lane + 32 * i;
+        if (e < a.K) grad[t * a.K + e] = value(i, gs[e]);
+      }
     }
     __syncwarp();
   }
@@ -550,15 +644,15 @@ int route_grid(int64_t n) {
 template <int NPL, bool BY_SCORE, typename T>
 so2_status run_route(const RouteArgs &a, int64_t n, const T *logits, const float *bias,
                      float *weights, int32_t *index, int32_t *counts, cudaStream_t s) {
-  const int smem = ROUTE_WARPS * route_words(a.K, a.n_groups, a.top_k) * 8 + a.K * 4;
+  const int smem = ROUTE_WARPS * route_words(a.K, a.n_groups, a.top_k, BY_SCORE) * 8 + a.K * 4;
   if (smem > 48 * 1024)
     MODEL_CK(cudaFuncSetAttribute(k_route<NPL, BY_SCORE, T>,
                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   // up to 16 rows one block stores the counts itself, without a clearing launch
   const int grid = n <= 16 ? 1 : route_grid(n);
   if (counts && grid > 1) MODEL_CK(cudaMemsetAsync(counts, 0, sizeof(int32_t) * a.K, s));
-  k_route<NPL, BY_SCORE, T><<<grid, 32 * ROUTE_WARPS, smem, s>>>(a, n, logits, bias, weights, index,
-                                                                 counts);
+  k_route<NPL, BY_SCORE, T><<<grid, 32 * ROUTE_WARPS, smem, s>>>(
+      a, n, logits, expert_vectors<NPL>(a.K, logits), bias, weights, index, counts);
   MODEL_CKL();
   return SO2_OK;
 }
@@ -575,11 +669,13 @@ so2_status run_route(const RouteArgs &a, int64_t n, const void *logits, const fl
 template <int NPL, typename T>
 so2_status run_route_grad(const RouteArgs &a, int64_t n, const T *logits, const int32_t *index,
                           const float *gw, float *grad, cudaStream_t s) {
-  const int smem = ROUTE_WARPS * a.K * 4, threads = 32 * ROUTE_WARPS;
+  const int threads = 32 * ROUTE_WARPS;
+  const bool vec = expert_vectors<NPL>(a.K, logits);
+  const bool out = NPL >= 4 && a.K % 4 == 0 && aligned_to(grad, 16);
   if (a.softmax && !a.renorm)
-    k_route_grad<NPL, true, T><<<route_grid(n), threads, smem, s>>>(a, n, logits, index, gw, grad);
+    k_route_grad<NPL, true, T><<<route_grid(n), threads, 0, s>>>(a, n, logits, vec, index, gw, grad, out);
   else
-    k_route_grad<NPL, false, T><<<route_grid(n), threads, smem, s>>>(a, n, logits, index, gw, grad);
+    k_route_grad<NPL, false, T><<<route_grid(n), threads, 0, s>>>(a, n, logits, vec, index, gw, grad, out);
   MODEL_CKL();
   return SO2_OK;
 }
