@@ -448,8 +448,26 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   float *gs = rows[w];
   constexpr int V = NPL >= 4 ? 4 : 1;
-  for (int64_t t = blockIdx.x * (int64_t)ROUTE_WARPS + w; t < n;
-       t += (int64_t)gridDim.x * ROUTE_WARPS) {
+  const int64_t step = (int64_t)gridDim.x * ROUTE_WARPS;
+  int64_t t = blockIdx.x * (int64_t)ROUTE_WARPS + w;
+  // A lane's first slot, read ahead: its expert and gradient two rows, its
+  // logit (and by FULL the row) one row before they are used, since the loads
+  // depend on one another and the work between them is short.
+  auto first = [&](int64_t r, int &e, float &g) {
+    e = -1, g = 0.f;
+    if (r < n && lane < a.top_k) {
+      e = index[r * a.top_k + lane];
+      g = gw[r * a.top_k + lane];
+      if (e < 0 || e >= a.K) e = -1, g = 0.f;
+    }
+  };
+  int e1, e2;
+  float g1, g2, v1 = 0.f, xn[NPL];
+  first(t, e1, g1);
+  first(t + step, e2, g2);
+  if (e1 >= 0) v1 = to_f32(logits[t * a.K + e1]);
+  if (FULL && t < n) load_experts<NPL>(logits + t * a.K, a.K, vec, xn);
+  for (; t < n; t += step) {
     const T *row = logits + t * a.K;
     auto slot = [&](int j, int &e, float &v, float &g) {
       e = j < a.top_k ? index[t * a.top_k + j] : -1;
@@ -457,12 +475,18 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
       if (e < 0 || e >= a.K) e = -1, g = 0.f;
       v = e >= 0 ? to_f32(row[e]) : 0.f;
     };
-    int e0;  // this lane's first slot; slots beyond 32 are read again below
-    float v0, g0;
-    slot(lane, e0, v0, g0);
+    const int e0 = e1;  // slots beyond 32 are read below
+    const float v0 = v1, g0 = g1;
     float x[NPL];
+    if (FULL) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) x[i] = xn[i];
+    }
+    e1 = e2, g1 = g2, v1 = 0.f;
+    if (e1 >= 0) v1 = to_f32(logits[(t + step) * a.K + e1]);
+    first(t + 2 * step, e2, g2);
+    if (FULL && t + step < n) load_experts<NPL>(logits + (t + step) * a.K, a.K, vec, xn);
     float m0 = 0.f, z = 1.f;
-    if (FULL) load_experts<NPL>(row, a.K, vec, x);
 #pragma unroll
     for (int i = 0; i < NPL; i += V) {
       float zero[V] = {};
