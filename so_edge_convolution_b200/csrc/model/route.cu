@@ -609,6 +609,91 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
   }
 }
 
+// The same without FULL and with at most 32 slots: a group of 2^SHIFT lanes a
+// row, one slot a lane, so a warp takes 32 >> SHIFT consecutive rows, builds
+// their gradients in shared memory (K each) and stores them in one piece.
+template <int SHIFT, typename T>
+__global__ void __launch_bounds__(32 * ROUTE_WARPS)
+    k_route_grad_slots(RouteArgs a, int64_t n, const T *__restrict__ logits,
+                       const int *__restrict__ index, const float *__restrict__ gw,
+                       float *__restrict__ grad, bool vec) {
+  extern __shared__ __align__(16) float gsm[];
+  constexpr int LANES = 1 << SHIFT, ROWS = 32 >> SHIFT;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int sub = lane & (LANES - 1), r = lane >> SHIFT;
+  const int size = (ROWS * a.K + 3) & ~3;
+  float *gs = gsm + w * size;
+  float *mine = gs + r * a.K;
+  auto sum = [&](float v) {
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  const int64_t step = (int64_t)gridDim.x * ROUTE_WARPS * ROWS;
+  int64_t t0 = (blockIdx.x * (int64_t)ROUTE_WARPS + w) * ROWS;
+  // the next rows' slots are read under this step's work
+  int en;
+  float gn;
+  auto read = [&](int64_t t) {
+    en = -1, gn = 0.f;
+    if (t < n && sub < a.top_k) {
+      en = index[t * a.top_k + sub];
+      gn = gw[t * a.top_k + sub];
+    }
+    if (en < 0 || en >= a.K) en = -1, gn = 0.f;
+  };
+  read(t0 + r);
+  for (; t0 < n; t0 += step) {
+    const int e = en;
+    const float g = gn;
+    const float v = e >= 0 ? to_f32(logits[(t0 + r) * a.K + e]) : 0.f;
+    read(t0 + step + r);
+    for (int i = lane * 4; i < size; i += 128)
+      *reinterpret_cast<float4 *>(gs + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    float s = 0.f, total = 1.f, d = g;
+    if (a.softmax) {  // renormalised
+      float mc = e >= 0 ? v : -INFINITY;
+#pragma unroll
+      for (int o = LANES / 2; o; o >>= 1) mc = fmaxf(mc, __shfl_xor_sync(0xffffffffu, mc, o));
+      if (e >= 0) s = expf(v - mc);
+    } else if (e >= 0) {
+      s = sigmoid_f(v);
+    }
+    if (a.renorm) {
+      total = sum(s);
+      if (total == 0.f) total = INFINITY;  // such scores weigh 0
+      const float p = s / total;           // (1 for a single slot, whose gradient is then 0)
+      d = g - sum(g * p);
+      if (a.softmax) d *= p;
+    }
+    d *= a.scale;
+    if (!a.softmax) d *= s * sigmoid_f(-v) / total;
+    // an expert named twice shows by its tag, and adds up in slot order
+    __syncwarp();
+    if (e >= 0) mine[e] = __int_as_float(lane);
+    __syncwarp();
+    const bool any = __any_sync(0xffffffffu, e >= 0 && __float_as_int(mine[e]) != lane);
+    __syncwarp();
+    if (e >= 0) mine[e] = any ? 0.f : d;
+    __syncwarp();
+    if (any)
+      for (int l = 0; l < LANES; ++l) {
+        if (sub == l && e >= 0) mine[e] += d;
+        __syncwarp();
+      }
+    const int64_t rows = n - t0 < ROWS ? n - t0 : ROWS;
+    const int have = (int)rows * a.K;
+    float *out = grad + t0 * a.K;
+    if (vec && have % 4 == 0) {
+      for (int i = lane * 4; i < have; i += 128)
+        *reinterpret_cast<float4 *>(out + i) = *reinterpret_cast<const float4 *>(gs + i);
+    } else {
+      for (int i = lane; i < have; i += 32) out[i] = gs[i];
+    }
+    __syncwarp();
+  }
+}
+
 }  // namespace so2
 
 using namespace so2;
@@ -690,16 +775,28 @@ so2_status run_route(const RouteArgs &a, int64_t n, const void *logits, const fl
   ROUTE_DISPATCH(a.K, return run_route<NPL, false, T>(a, n, x, bias, weights, index, counts, s))
 }
 
-template <int NPL, typename T>
+template <int NPL, bool FULL, typename T>
 so2_status run_route_grad(const RouteArgs &a, int64_t n, const T *logits, const int32_t *index,
                           const float *gw, float *grad, cudaStream_t s) {
-  const int threads = 32 * ROUTE_WARPS;
-  const bool vec = expert_vectors<NPL>(a.K, logits);
-  const bool out = NPL >= 4 && a.K % 4 == 0 && aligned_to(grad, 16);
-  if (a.softmax && !a.renorm)
-    k_route_grad<NPL, true, T><<<route_grid(n), threads, 0, s>>>(a, n, logits, vec, index, gw, grad, out);
-  else
-    k_route_grad<NPL, false, T><<<route_grid(n), threads, 0, s>>>(a, n, logits, vec, index, gw, grad, out);
+  k_route_grad<NPL, FULL, T><<<route_grid(n), 32 * ROUTE_WARPS, 0, s>>>(
+      a, n, logits, expert_vectors<NPL>(a.K, logits), index, gw, grad,
+      NPL >= 4 && a.K % 4 == 0 && aligned_to(grad, 16));
+  MODEL_CKL();
+  return SO2_OK;
+}
+
+template <int SHIFT, typename T>
+so2_status run_route_grad_slots(const RouteArgs &a, int64_t n, const T *logits,
+                                const int32_t *index, const float *gw, float *grad, cudaStream_t s) {
+  constexpr int ROWS = 32 >> SHIFT;
+  const int smem = ROUTE_WARPS * ((ROWS * a.K + 3) & ~3) * 4;
+  if (smem > 48 * 1024)
+    MODEL_CK(cudaFuncSetAttribute(k_route_grad_slots<SHIFT, T>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  // a step's rows start on a vector's boundary if one row does, or four of them
+  const bool vec = aligned_to(grad, 16) && (ROWS * a.K) % 4 == 0;
+  k_route_grad_slots<SHIFT, T><<<route_grid(ceil_div(n, ROWS)), 32 * ROUTE_WARPS, smem, s>>>(
+      a, n, logits, index, gw, grad, vec);
   MODEL_CKL();
   return SO2_OK;
 }
@@ -708,7 +805,13 @@ template <typename T>
 so2_status run_route_grad(const RouteArgs &a, int64_t n, const void *logits, const int32_t *index,
                           const float *gw, float *grad, cudaStream_t s) {
   const T *x = static_cast<const T *>(logits);
-  ROUTE_DISPATCH(a.K, return run_route_grad<NPL, T>(a, n, x, index, gw, grad, s))
+  if (a.softmax && !a.renorm)
+    ROUTE_DISPATCH(a.K, return run_route_grad<NPL, true, T>(a, n, x, index, gw, grad, s))
+  if (a.top_k <= 4) return run_route_grad_slots<2, T>(a, n, x, index, gw, grad, s);
+  if (a.top_k <= 8) return run_route_grad_slots<3, T>(a, n, x, index, gw, grad, s);
+  if (a.top_k <= 16) return run_route_grad_slots<4, T>(a, n, x, index, gw, grad, s);
+  if (a.top_k <= 32) return run_route_grad_slots<5, T>(a, n, x, index, gw, grad, s);
+  ROUTE_DISPATCH(a.K, return run_route_grad<NPL, false, T>(a, n, x, index, gw, grad, s))
 }
 
 }  // namespace
