@@ -47,12 +47,12 @@ __device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + expf(-
 
 constexpr int ROUTE_WARPS = 4;
 
-// The order of a row by scores in 64 bits: rank[e] is K for the first expert
+// The order of a row by scores (or logits) in 64 bits: rank[e] is K for the first expert
 // down to 1, or 0 if it may not be chosen.  All lanes of the warp call; keys
 // (K + n_groups words) and rank (K words) are the warp's shared memory, and
 // nothing of the caller's is passed in registers, so that the usual path does
 // not pay for this one.
-template <typename T>
+template <bool BY_SCORE, typename T>
 __device__ __noinline__ void rank_in_64_bits(const RouteArgs &a, const T *__restrict__ row, float m0,
                                              const float *__restrict__ bias, uint64_t *keys,
                                              uint32_t *rank) {
@@ -61,13 +61,14 @@ __device__ __noinline__ void rank_in_64_bits(const RouteArgs &a, const T *__rest
   double *cs = reinterpret_cast<double *>(keys);
   __syncwarp();
   double z = 0.0;
-  if (a.softmax) {
+  if (BY_SCORE && a.softmax) {
     for (int e = lane; e < a.K; e += 32) z += exp((double)to_f32(row[e]) - m0);
     z = warp_sum(z);
   }
   for (int e = lane; e < a.K; e += 32) {
     const double x = to_f32(row[e]);
-    double c = a.softmax ? exp(x - m0) / z : 1.0 / (1.0 + exp(-x));
+    double c = x;
+    if (BY_SCORE) c = a.softmax ? exp(x - m0) / z : 1.0 / (1.0 + exp(-x));
     if (bias) c += bias[e];
     cs[e] = x == -INFINITY ? -INFINITY : c;
   }
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
 
     if (a.top_k == a.K) {  // nothing to select: slot e is expert e
       if (again) {  // (only to know which experts may not be chosen)
-        rank_in_64_bits(a, row, m0, bias, keys, rank);
+        rank_in_64_bits<true>(a, row, m0, bias, keys, rank);
 #pragma unroll
         for (int i = 0; i < NPL; ++i) key[i] = lane * NPL + i < a.K ? rank[lane * NPL + i] : 0;
       }
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
 
     for (;;) {
       if (again) {
-        rank_in_64_bits(a, row, m0, bias, keys, rank);
+        rank_in_64_bits<true>(a, row, m0, bias, keys, rank);
 #pragma unroll
         for (int i = 0; i < NPL; ++i) key[i] = lane * NPL + i < a.K ? rank[lane * NPL + i] : 0;
       }
@@ -424,6 +425,294 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
       if (counts && e >= 0) atomicAdd(&hist[e], 1);
       weights[t * a.top_k + j] = e < 0 ? 0.f : (j == lane ? s0 : score(to_f32(row[e]))) * f;
       index[t * a.top_k + j] = e;
+    }
+    __syncwarp();
+  }
+  if (counts) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.K; e += blockDim.x) {
+      if (gridDim.x == 1) counts[e] = hist[e];
+      else if (hist[e]) atomicAdd(&counts[e], hist[e]);
+    }
+  }
+}
+
+// ---- at most eight slots of at most 256 experts -----------------------------------
+// A group of 2^SHIFT lanes a row, NPL experts a lane, so a warp takes several
+// rows.  The expert's index replaces the low bits of its key, which makes the
+// words distinct, ties in index order, and an exchange of a sorting network
+// two instructions: each lane sorts its words, and SHIFT butterfly steps merge
+// the lanes' best eight.  Keys that differ only in the replaced bits (2^-15 of
+// a value at 256 experts) and, by score, scores that f32 cannot tell apart
+// send the row to rank_in_64_bits: about one row in a hundred.
+__device__ __forceinline__ void exchange(uint32_t &a, uint32_t &b) {
+  const uint32_t hi = a > b ? a : b;
+  b = a > b ? b : a;
+  a = hi;
+}
+// Falling order of eight words that rise and fall, or fall and rise.
+__device__ __forceinline__ void sort_bitonic8(uint32_t (&l)[8]) {
+#pragma unroll
+  for (int d = 4; d; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & d)) exchange(l[i], l[i + d]);
+}
+// Falling order of N words (Batcher's odd-even merge sort).
+template <int N>
+__device__ __forceinline__ void sort_words(uint32_t *l) {
+#pragma unroll
+  for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+    for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p))
+            exchange(l[i + j], l[i + j + k]);
+}
+// The eight best of two sorted lists, sorted, into the first.
+__device__ __forceinline__ void merge8(uint32_t (&l)[8], const uint32_t (&o)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) l[i] = l[i] > o[7 - i] ? l[i] : o[7 - i];
+  sort_bitonic8(l);
+}
+
+__host__ __device__ inline int route_top_words(int K, int n_groups, int rows) {
+  const int f32s = n_groups > 1 ? (rows * (K + n_groups) + 1) / 2 : 0;
+  const int slow = K + n_groups + (K + 1) / 2;  // rank_in_64_bits
+  return (f32s > slow ? f32s : slow) + rows * 4;
+}
+
+template <int SHIFT, int NPL, bool BY_SCORE, typename T>
+__global__ void __launch_bounds__(32 * ROUTE_WARPS)
+    k_route_top(RouteArgs a, int64_t n, const T *__restrict__ logits, bool vec,
+                const float *__restrict__ bias, float *__restrict__ weights,
+                int *__restrict__ index, int *__restrict__ counts) {
+  extern __shared__ uint64_t sm[];
+  constexpr int LANES = 1 << SHIFT, ROWS = 32 >> SHIFT, IDX = LANES * NPL;  // indices of a word
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int sub = lane & (LANES - 1), r = lane >> SHIFT;
+  const int words = route_top_words(a.K, a.n_groups, ROWS);
+  uint64_t *keys = sm + w * words;
+  int *chosen = reinterpret_cast<int *>(keys + words - ROWS * 4);  // [ROWS][8]
+  float *cs = reinterpret_cast<float *>(keys) + r * (a.K + a.n_groups);
+  uint32_t *rank = reinterpret_cast<uint32_t *>(keys + a.K + a.n_groups);
+  int *hist = reinterpret_cast<int *>(sm + ROUTE_WARPS * words);
+  if (counts) {
+    for (int e = threadIdx.x; e < a.K; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+  }
+  auto row_max = [&](float v) {
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  };
+  auto row_sum = [&](float v) {
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  const unsigned row_lanes = (LANES == 32 ? 0xffffffffu : (1u << (LANES & 31)) - 1) << (r * LANES);
+  auto row_any = [&](bool v) { return (__ballot_sync(0xffffffffu, v) & row_lanes) != 0; };
+  const bool grouped = a.top_groups < a.n_groups;
+  constexpr int V = NPL * sizeof(T) <= 16 ? NPL : 16 / (int)sizeof(T);
+  auto load = [&](int64_t t, float(&x)[NPL]) {
+    const T *p = logits + t * a.K;
+#pragma unroll
+    for (int i = 0; i < NPL; i += V) {
+      const int e = sub * NPL + i;
+      if (vec && t < n && e < a.K) {
+        if constexpr (V >= 4) {
+          float q[V];
+          load_vec<V>(p + e, q);
+#pragma unroll
+          for (int v = 0; v < V; ++v) x[i + v] = q[v];
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[i + v] = t < n && e + v < a.K ? to_f32(p[e + v]) : -INFINITY;
+      }
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * ROUTE_WARPS * ROWS;
+  int64_t t0 = (blockIdx.x * (int64_t)ROUTE_WARPS + w) * ROWS;
+  float x[NPL], xn[NPL];
+  load(t0 + r, xn);
+  for (; t0 < n; t0 += step) {
+    const int64_t t = t0 + r;
+    const T *row = logits + t * a.K;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) x[i] = xn[i];
+    load(t + step, xn);
+    float m0 = 0.f, z = 1.f;
+    if (a.softmax && (BY_SCORE || !a.renorm)) {
+      m0 = x[0];
+#pragma unroll
+      for (int i = 1; i < NPL; ++i) m0 = fmaxf(m0, x[i]);
+      m0 = row_max(m0);
+      if (m0 == -INFINITY) m0 = 0.f;
+      z = 0.f;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) z += expf(x[i] - m0);
+      z = row_sum(z);
+    }
+    // words, and by score the scores for a second look at what is near
+    uint32_t l[NPL];
+    float c[NPL];
+    float size = 0.f;
+    bool again = false;
+    const float iz = BY_SCORE && a.softmax ? 1.f / z : 1.f;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      const int e = sub * NPL + i;
+      const bool dead = x[i] == -INFINITY;
+      c[i] = x[i];
+      if (BY_SCORE) {
+        const float s = a.softmax ? expf(x[i] - m0) * iz : sigmoid_f(x[i]);
+        c[i] = s + (bias && e < a.K ? bias[e] : 0.f);
+        if (dead) c[i] = -INFINITY;
+        else if (c[i] != -INFINITY) size = fmaxf(size, fmaxf(s, fabsf(c[i])));
+      }
+      again |= c[i] != c[i];  // NaN is left to the second look
+      const uint32_t k = order_key32(bias || !BY_SCORE ? c[i] : x[i], dead || c[i] == -INFINITY);
+      l[i] = k < IDX ? 0 : (k & ~(uint32_t)(IDX - 1)) | (uint32_t)(IDX - 1 - e);
+      if (grouped && e < a.K) cs[e] = c[i];
+    }
+    float tol = 0.f;
+    if (BY_SCORE) tol = row_max(size) * ROUTE_NEAR;
+    if (grouped) {
+      __syncwarp();
+      uint32_t *gk = reinterpret_cast<uint32_t *>(cs + a.K);
+      for (int g = sub; g < a.n_groups; g += LANES) {
+        float b0 = -INFINITY, b1 = -INFINITY;
+        for (int j = 0; j < a.per; ++j) {
+          const float v = cs[g * a.per + j];
+          b1 = fmaxf(b1, fminf(b0, v));
+          b0 = fmaxf(b0, v);
+        }
+        gk[g] = order_key32(a.group_top > 1 && b1 != -INFINITY ? b0 + b1 : b0, b0 == -INFINITY);
+      }
+      __syncwarp();
+      uint32_t floor_key = 0xffffffffu, next_key = 0;  // the last group that stays, the first that does not
+      for (int g = sub; g < a.n_groups; g += LANES) {
+        const uint32_t k = gk[g];
+        int before = 0;
+        for (int h = 0; h < a.n_groups; ++h) before += gk[h] > k || (gk[h] == k && h < g);
+        if (before == a.top_groups - 1) floor_key = k;
+        if (before == a.top_groups) next_key = k;
+        cs[g] = before < a.top_groups ? 1.f : 0.f;  // (the scores are not read any more)
+      }
+      __syncwarp();
+      if (BY_SCORE) {
+#pragma unroll
+        for (int o = LANES / 2; o; o >>= 1) {
+          const uint32_t f = __shfl_xor_sync(0xffffffffu, floor_key, o);
+          const uint32_t m = __shfl_xor_sync(0xffffffffu, next_key, o);
+          floor_key = f < floor_key ? f : floor_key;
+          next_key = m > next_key ? m : next_key;
+        }
+        if (next_key > 1) again |= !(key_value(floor_key) - key_value(next_key) > 2.f * tol);
+      }
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        const int e = sub * NPL + i;
+        if (e < a.K && cs[e / a.per] == 0.f) l[i] = 0, c[i] = -INFINITY;
+      }
+      __syncwarp();
+    }
+    // the row's eight best words, in every lane of the group
+    uint32_t top[8];
+    if constexpr (NPL == 16) {
+      uint32_t o[8];
+      uint32_t q[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) q[i] = l[i];
+      sort_words<8>(q);
+      sort_words<8>(q + 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top[i] = q[i], o[i] = q[8 + i];
+      merge8(top, o);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top[i] = i < NPL ? l[i < NPL ? i : 0] : 0;
+      sort_words<(NPL < 8 ? NPL : 8)>(top);
+    }
+#pragma unroll
+    for (int d = 1; d < LANES; d <<= 1) {
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = __shfl_xor_sync(0xffffffffu, top[i], d);
+      merge8(top, o);
+    }
+    // slot `sub` of the row, its logit and (by score) its c
+    uint32_t word = 0, last = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i == sub) word = top[i];
+      if (i == a.top_k - 1) last = top[i];
+    }
+    int e = sub < a.top_k && word != 0 ? IDX - 1 - (int)(word & (IDX - 1)) : -1;
+    float v = e >= 0 ? to_f32(row[e]) : 0.f;
+    const float b = BY_SCORE && bias && e >= 0 ? bias[e] : 0.f;
+    {
+      // neighbours whose words do not tell them apart, unless they are equal
+      const uint32_t wn = __shfl_down_sync(0xffffffffu, word, 1);
+      const float vn = __shfl_down_sync(0xffffffffu, v, 1), bn = __shfl_down_sync(0xffffffffu, b, 1);
+      const uint32_t bits = ~(uint32_t)(IDX - 1);
+      if (sub + 1 < a.top_k && e >= 0 && wn != 0) {
+        bool close = (word & bits) == (wn & bits);
+        if (BY_SCORE && bias) close |= !(key_value(word & bits) - key_value((wn & bits) | (IDX - 1)) > tol);
+        again |= close && !(v == vn && b == bn);
+      }
+      // the last one chosen and those left over
+      const int from = r * LANES + a.top_k - 1;
+      const float vl = __shfl_sync(0xffffffffu, v, from), bl = __shfl_sync(0xffffffffu, b, from);
+      const float cut = last ? key_value(last & bits) - tol : INFINITY;
+      bool close = false;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        close |= l[i] != 0 && l[i] < last &&
+                 ((l[i] & bits) == (last & bits) || (BY_SCORE && bias && !(c[i] < cut)));
+      if (close) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+          if (l[i] != 0 && l[i] < last &&
+              ((l[i] & bits) == (last & bits) || (BY_SCORE && bias && !(c[i] < cut))))
+            again |= !(x[i] == vl && (!BY_SCORE || !bias || bias[sub * NPL + i] == bl));
+      }
+    }
+    again = row_any(again) && t < n;
+    for (unsigned m = __ballot_sync(0xffffffffu, again && sub == 0); m; m &= m - 1) {
+      const int from = __ffs(m) - 1, rr = from >> SHIFT;
+      const float mr = __shfl_sync(0xffffffffu, m0, from);
+      rank_in_64_bits<BY_SCORE>(a, logits + (t0 + rr) * a.K, mr, bias, keys, rank);
+      if (lane < 8) chosen[rr * 8 + lane] = -1;
+      __syncwarp();
+      for (int q = lane; q < a.K; q += 32)
+        if (rank[q] != 0 && a.K - (int)rank[q] < a.top_k) chosen[rr * 8 + a.K - rank[q]] = q;
+      __syncwarp();
+    }
+    if (again) {
+      e = sub < a.top_k ? chosen[r * 8 + sub] : -1;
+      v = e >= 0 ? to_f32(row[e]) : 0.f;
+    }
+    float s = 0.f;
+    if (a.softmax && a.renorm) {
+      const float mc = row_max(e >= 0 ? v : -INFINITY);
+      if (e >= 0) s = expf(v - mc);
+    } else if (e >= 0) {
+      s = a.softmax ? expf(v - m0) / z : sigmoid_f(v);
+    }
+    if (a.renorm) {
+      const float total = row_sum(s);
+      s = total == 0.f ? 0.f : s / total;
+    }
+    if (t < n && sub < a.top_k) {
+      weights[t * a.top_k + sub] = s * a.scale;
+      index[t * a.top_k + sub] = e;
+      if (counts && e >= 0) atomicAdd(&hist[e], 1);
     }
     __syncwarp();
   }
@@ -766,11 +1055,42 @@ so2_status run_route(const RouteArgs &a, int64_t n, const T *logits, const float
   return SO2_OK;
 }
 
+template <int SHIFT, int NPL, bool BY_SCORE, typename T>
+so2_status run_route_top(const RouteArgs &a, int64_t n, const T *logits, const float *bias,
+                         float *weights, int32_t *index, int32_t *counts, cudaStream_t s) {
+  constexpr int ROWS = 32 >> SHIFT;
+  const int smem = ROUTE_WARPS * route_top_words(a.K, a.n_groups, ROWS) * 8 + a.K * 4;
+  if (smem > 48 * 1024)
+    MODEL_CK(cudaFuncSetAttribute(k_route_top<SHIFT, NPL, BY_SCORE, T>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  const int grid = n <= 16 ? 1 : route_grid(ceil_div(n, ROWS));
+  if (counts && grid > 1) MODEL_CK(cudaMemsetAsync(counts, 0, sizeof(int32_t) * a.K, s));
+  constexpr int V = NPL * sizeof(T) <= 16 ? NPL : 16 / (int)sizeof(T);
+  const bool vec = V >= 4 && a.K % V == 0 && aligned_to(logits, V * sizeof(T));
+  k_route_top<SHIFT, NPL, BY_SCORE, T><<<grid, 32 * ROUTE_WARPS, smem, s>>>(
+      a, n, logits, vec, bias, weights, index, counts);
+  MODEL_CKL();
+  return SO2_OK;
+}
+
+template <bool BY_SCORE, typename T>
+so2_status run_route_top(const RouteArgs &a, int64_t n, const T *x, const float *bias,
+                         float *weights, int32_t *index, int32_t *counts, cudaStream_t s) {
+  if (a.K <= 32) return run_route_top<3, 4, BY_SCORE, T>(a, n, x, bias, weights, index, counts, s);
+  if (a.K <= 64) return run_route_top<3, 8, BY_SCORE, T>(a, n, x, bias, weights, index, counts, s);
+  if (a.K <= 128) return run_route_top<3, 16, BY_SCORE, T>(a, n, x, bias, weights, index, counts, s);
+  return run_route_top<4, 16, BY_SCORE, T>(a, n, x, bias, weights, index, counts, s);
+}
+
 template <typename T>
 so2_status run_route(const RouteArgs &a, int64_t n, const void *logits, const float *bias,
                      float *weights, int32_t *index, int32_t *counts, cudaStream_t s) {
   const T *x = static_cast<const T *>(logits);
-  if (bias || (a.top_groups < a.n_groups && a.group_top > 1))
+  const bool by_score = bias || (a.top_groups < a.n_groups && a.group_top > 1);
+  if (a.top_k <= 8 && a.top_k < a.K && a.K <= 256)
+    return by_score ? run_route_top<true, T>(a, n, x, bias, weights, index, counts, s)
+                    : run_route_top<false, T>(a, n, x, bias, weights, index, counts, s);
+  if (by_score)
     ROUTE_DISPATCH(a.K, return run_route<NPL, true, T>(a, n, x, bias, weights, index, counts, s))
   ROUTE_DISPATCH(a.K, return run_route<NPL, false, T>(a, n, x, bias, weights, index, counts, s))
 }
