@@ -493,33 +493,40 @@ def _torch_dtype(code):
     return _TORCH_DTYPE[code]
 
 
+_SMALL_WS = {}  # (device index, stream) -> workspace of the calls that need a status word or little more
+_SMALL_WS_BYTES = 4096
+
+
 def _model_ws(need, where, device, ws):
-    """The workspace of one model operator call: the caller's, or a new one
-    from torch's allocator, which belongs to the current stream or to the
-    graph being captured; check() reads the last such call's status."""
+    """The workspace of one model operator call: the caller's; or, small, one
+    of the current stream's own that is kept; or a new one from torch's
+    allocator, which belongs to the stream, or to the graph being captured.
+    check() reads the last such call's status."""
     if need == 0:
         raise So2Error(2, where)
     if ws:
         return ws.get(need)
-    w = Workspace(device)
-    _MODEL_WS[_device(device)] = w
+    if need <= _SMALL_WS_BYTES and not torch.cuda.is_current_stream_capturing():
+        key = (device.index, _stream(device).value)
+        w = _SMALL_WS.get(key)
+        if w is None:
+            w = _SMALL_WS[key] = Workspace(device)
+            w.get(_SMALL_WS_BYTES)
+    else:
+        w = Workspace(device)
+    _MODEL_WS[device] = w
     return w.get(need)
 
 
-class _on:
-    """The tensors' device made current for a call, if it is another one."""
-
-    def __init__(self, device):
-        self.other = (torch.cuda.device(device)
-                      if torch.cuda.current_device() != device.index else None)
-
-    def __enter__(self):
-        if self.other is not None:
-            self.other.__enter__()
-
-    def __exit__(self, *exc):
-        if self.other is not None:
-            self.other.__exit__(*exc)
+def _run(dev, where, call, *args):
+    """One library call on the current stream of the tensors' device, which is
+    made current for it if another one is."""
+    if torch.cuda.current_device() == dev.index:
+        code = call(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            code = call(*args, _stream(dev))
+    _check_call(code, where)
 
 
 def _need(t, name, shape, dtype, device=None):
@@ -536,14 +543,14 @@ def _on_device(t, name, device):
         raise ValueError(f"{name} must be on {device or 'a CUDA device'}, not {t.device}")
 
 
-def _given_out(out, name, shape, dtype, device):
-    """A caller's output (checked: written in place) or a new one."""
+def _given_out(out, name, shape, dtype, like):
+    """A caller's output (checked: written in place) or a new one beside `like`."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if (tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device
+        return like.new_empty(shape, dtype=dtype)
+    if (out.shape != shape or out.dtype != dtype or out.device != like.device
             or not out.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
-                         f"on {device}")
+                         f"on {like.device}")
     return out
 
 
@@ -574,16 +581,14 @@ def embed_forward(desc, ids, table, out=None, ws=None):
                   dev)
     shape, dt = (n, desc.n_comp, desc.channels), _torch_dtype(desc.out_dtype)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
-    elif tuple(out.shape) != shape or out.dtype != dt or out.device != dev:
+        out = ids.new_empty(shape, dtype=dt)
+    elif out.shape != shape or out.dtype != dt or out.device != dev:
         raise ValueError(f"out must be {dt} of shape {shape} on {dev}")
     ld = _rows_of(out, n, desc.n_comp * desc.channels, "out")
-    with _on(dev):
-        need = int(lib.so2conv_embed_workspace_size(ctypes.byref(desc), n, WS_FORWARD))
-        p, nb = _model_ws(need, "embed_workspace_size", dev, ws)
-        code = lib.so2conv_embed_forward(ctypes.byref(desc), n, _ptr(ids), _ptr(table),
-                                         out.data_ptr(), ld, p, nb, _stream(dev))
-    _check_call(code, "so2conv_embed_forward")
+    need = lib.so2conv_embed_workspace_size(ctypes.byref(desc), n, WS_FORWARD)
+    p, nb = _model_ws(need, "embed_workspace_size", dev, ws)
+    _run(dev, "so2conv_embed_forward", lib.so2conv_embed_forward, ctypes.byref(desc), n, _ptr(ids),
+         _ptr(table), out.data_ptr(), ld, p, nb)
     return out
 
 
@@ -606,13 +611,11 @@ def embed_backward(desc, ids, grad_out, out=None, ws=None):
     if n > 1 and grad_out.stride(0) < desc.channels:  # rows that overlap (an expanded tensor)
         grad_out = grad_out.contiguous()
     ld = desc.channels if n <= 1 else grad_out.stride(0)
-    out = _given_out(out, "out", (desc.n_rows, desc.channels), torch.float32, dev)
-    with _on(dev):
-        need = int(lib.so2conv_embed_workspace_size(ctypes.byref(desc), n, WS_BACKWARD))
-        p, nb = _model_ws(need, "embed_workspace_size", dev, ws)
-        code = lib.so2conv_embed_backward(ctypes.byref(desc), n, _ptr(ids), grad_out.data_ptr(),
-                                          ld, _ptr(out), p, nb, _stream(dev))
-    _check_call(code, "so2conv_embed_backward")
+    out = _given_out(out, "out", (desc.n_rows, desc.channels), torch.float32, ids)
+    need = lib.so2conv_embed_workspace_size(ctypes.byref(desc), n, WS_BACKWARD)
+    p, nb = _model_ws(need, "embed_workspace_size", dev, ws)
+    _run(dev, "so2conv_embed_backward", lib.so2conv_embed_backward, ctypes.byref(desc), n,
+         _ptr(ids), grad_out.data_ptr(), ld, _ptr(out), p, nb)
     return out
 
 
@@ -631,13 +634,11 @@ def route_forward(desc, logits, bias=None):
     dev = logits.device
     if bias is not None:
         bias = _need(bias, "bias", (desc.n_experts,), torch.float32, dev)
-    weights = torch.empty((n, desc.top_k), dtype=torch.float32, device=dev)
-    index = torch.empty((n, desc.top_k), dtype=torch.int32, device=dev)
-    counts = torch.empty(desc.n_experts, dtype=torch.int32, device=dev)
-    with _on(dev):
-        code = lib.so2conv_route_forward(ctypes.byref(desc), n, _ptr(logits), _ptr(bias),
-                                         _ptr(weights), _ptr(index), _ptr(counts), _stream(dev))
-    _check_call(code, "so2conv_route_forward")
+    weights = logits.new_empty((n, desc.top_k), dtype=torch.float32)
+    index = torch.empty_like(weights, dtype=torch.int32)
+    counts = index.new_empty(desc.n_experts)
+    _run(dev, "so2conv_route_forward", lib.so2conv_route_forward, ctypes.byref(desc), n,
+         _ptr(logits), _ptr(bias), _ptr(weights), _ptr(index), _ptr(counts))
     return weights, index, counts
 
 
@@ -649,11 +650,9 @@ def route_backward(desc, logits, index, grad_weights, out=None):
     dev = logits.device
     index = _need(index, "index", (n, desc.top_k), torch.int32, dev)
     grad_weights = _need(grad_weights, "grad_weights", (n, desc.top_k), torch.float32, dev)
-    out = _given_out(out, "out", (n, desc.n_experts), torch.float32, dev)
-    with _on(dev):
-        code = lib.so2conv_route_backward(ctypes.byref(desc), n, _ptr(logits), _ptr(index),
-                                          _ptr(grad_weights), _ptr(out), _stream(dev))
-    _check_call(code, "so2conv_route_backward")
+    out = _given_out(out, "out", (n, desc.n_experts), torch.float32, logits)
+    _run(dev, "so2conv_route_backward", lib.so2conv_route_backward, ctypes.byref(desc), n,
+         _ptr(logits), _ptr(index), _ptr(grad_weights), _ptr(out))
     return out
 
 
@@ -677,14 +676,11 @@ def mix_experts_forward(desc, experts, weights, index=None, out=None, ws=None):
     """so2conv_mix_experts_forward: out [n_systems, n_weights] of out_dtype."""
     lib = load()
     n, dev, experts, weights, index = _mix_inputs(desc, experts, weights, index)
-    out = _given_out(out, "out", (n, desc.n_weights), _torch_dtype(desc.out_dtype), dev)
-    with _on(dev):
-        need = int(lib.so2conv_mix_workspace_size(ctypes.byref(desc), n, WS_FORWARD))
-        p, nb = _model_ws(need, "mix_workspace_size", dev, ws)
-        code = lib.so2conv_mix_experts_forward(ctypes.byref(desc), n, _ptr(experts),
-                                               _ptr(weights), _ptr(index), _ptr(out), p, nb,
-                                               _stream(dev))
-    _check_call(code, "so2conv_mix_experts_forward")
+    out = _given_out(out, "out", (n, desc.n_weights), _torch_dtype(desc.out_dtype), experts)
+    need = lib.so2conv_mix_workspace_size(ctypes.byref(desc), n, WS_FORWARD)
+    p, nb = _model_ws(need, "mix_workspace_size", dev, ws)
+    _run(dev, "so2conv_mix_experts_forward", lib.so2conv_mix_experts_forward, ctypes.byref(desc), n,
+         _ptr(experts), _ptr(weights), _ptr(index), _ptr(out), p, nb)
     return out
 
 
@@ -699,14 +695,11 @@ def mix_experts_backward(desc, experts, weights, grad_out, index=None, need=None
     need = set(names if need is None else need)
     shapes = {"grad_experts": (desc.n_experts, desc.n_weights), "grad_weights": (n, desc.top_k)}
     outs = _outputs(names, need, shapes, out, dict(dtype=torch.float32, device=dev))
-    with _on(dev):
-        size = int(lib.so2conv_mix_workspace_size(ctypes.byref(desc), n, WS_BACKWARD))
-        p, nb = _model_ws(size, "mix_workspace_size", dev, ws)
-        code = lib.so2conv_mix_experts_backward(ctypes.byref(desc), n, _ptr(experts),
-                                                _ptr(weights), _ptr(index), _ptr(grad_out),
-                                                *[_ptr(outs[k]) for k in names], p, nb,
-                                                _stream(dev))
-    _check_call(code, "so2conv_mix_experts_backward")
+    size = lib.so2conv_mix_workspace_size(ctypes.byref(desc), n, WS_BACKWARD)
+    p, nb = _model_ws(size, "mix_workspace_size", dev, ws)
+    _run(dev, "so2conv_mix_experts_backward", lib.so2conv_mix_experts_backward, ctypes.byref(desc),
+         n, _ptr(experts), _ptr(weights), _ptr(index), _ptr(grad_out),
+         *[_ptr(outs[k]) for k in names], p, nb)
     return {k: t for k, t in outs.items() if t is not None}
 
 
@@ -728,9 +721,7 @@ def dropout(desc, x, rng, residual=None, rows=None, out=None):
         residual = _need(residual, "residual", shape, dt, dev)
     if rows is not None:
         rows = _need(rows, "rows", (n,), torch.int64, dev)
-    out = _given_out(out, "out", shape, dt, dev)
-    with _on(dev):
-        code = lib.so2conv_dropout(ctypes.byref(desc), n, _ptr(x), _ptr(residual), _ptr(rows),
-                                   _ptr(rng), _ptr(out), _stream(dev))
-    _check_call(code, "so2conv_dropout")
+    out = _given_out(out, "out", shape, dt, x)
+    _run(dev, "so2conv_dropout", lib.so2conv_dropout, ctypes.byref(desc), n, _ptr(x),
+         _ptr(residual), _ptr(rows), _ptr(rng), _ptr(out))
     return out

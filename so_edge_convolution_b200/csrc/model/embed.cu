@@ -252,6 +252,13 @@ __global__ void __launch_bounds__(256)
     for (int u = 0; u < RUN_ROWS; ++u)
       if (k[u] < n_rows) load_vec<V>(grad + (int64_t)p[u] * ld + c, g[u]);
     if (j + RUN_ROWS < b) read(j + RUN_ROWS, kn, pn);
+    if (k[0] == cur && k[RUN_ROWS - 1] == cur) {  // eight of one run: their sum first
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        acc[v] += ((g[0][v] + g[1][v]) + (g[2][v] + g[3][v])) +
+                  ((g[4][v] + g[5][v]) + (g[6][v] + g[7][v]));
+      continue;
+    }
 #pragma unroll
     for (int u = 0; u < RUN_ROWS; ++u) {
       if (k[u] != cur) {
@@ -276,12 +283,21 @@ __global__ void __launch_bounds__(256)
 // sixteenth range from the w-th on.
 constexpr int JOIN_RANGES = 32, JOIN_WARPS = 16, JOIN_ALONE = 32;
 
+// (Thousands of partial sums of a frequent element's rows: added in 64 bits,
+// so that the error stays that of the ranges' own sums.)
 template <int V>
-__device__ __forceinline__ void join_add(float (&acc)[V], const float *from) {
+__device__ __forceinline__ void join_add(double (&acc)[V], const float *from) {
   float g[V];
   load_vec<V>(from, g);
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] += g[v];
+}
+template <int V>
+__device__ __forceinline__ void join_store(const double (&acc)[V], float scale, float *to) {
+  float r[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) r[v] = (float)(acc[v] * scale);
+  store_vec<V>(to, r);
 }
 
 template <int V>
@@ -289,7 +305,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS)
     k_embed_join(int64_t n, int64_t n_ranges, int len, const uint32_t *__restrict__ keys,
                  uint32_t n_rows, int channels, float scale, float *__restrict__ table,
                  const float *__restrict__ head, const float *__restrict__ tail) {
-  __shared__ float part[JOIN_WARPS][32 * V];
+  __shared__ double part[JOIN_WARPS][32 * V];
   __shared__ int64_t last[JOIN_RANGES];  // of long runs: the last range that starts in it
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = (blockIdx.y * 32 + lane) * V;
@@ -323,24 +339,20 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS)
     if (lo - r > JOIN_ALONE) {
       if (lane == 0) last[r - r0] = lo;
     } else if (c < channels) {
-      float acc[V];
-      load_vec<V>(tail + r * channels + c, acc);
+      double acc[V] = {};
+      join_add<V>(acc, tail + r * channels + c);
 #pragma unroll 4
       for (int64_t q = r + 1; q <= lo; ++q) join_add<V>(acc, head + q * channels + c);
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] *= scale;
-      store_vec<V>(table + (int64_t)key * channels + c, acc);
+      join_store<V>(acc, scale, table + (int64_t)key * channels + c);
     }
   }
   __syncthreads();
   for (unsigned m = todo; m; m &= m - 1) {
     const int64_t r = r0 + __ffs(m) - 1, lo = last[r - r0];
     if (lo < 0) continue;
-    float acc[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    double acc[V] = {};
     if (c < channels) {
-      if (w == 0) load_vec<V>(tail + r * channels + c, acc);
+      if (w == 0) join_add<V>(acc, tail + r * channels + c);
 #pragma unroll 8
       for (int64_t q = r + 1 + w; q <= lo; q += JOIN_WARPS) join_add<V>(acc, head + q * channels + c);
     }
@@ -350,12 +362,11 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS)
     if (w == 0 && c < channels) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float s = 0.f;
+        acc[v] = 0.0;
 #pragma unroll
-        for (int i = 0; i < JOIN_WARPS; ++i) s += part[i][lane * V + v];
-        acc[v] = s * scale;
+        for (int i = 0; i < JOIN_WARPS; ++i) acc[v] += part[i][lane * V + v];
       }
-      store_vec<V>(table + (int64_t)keys[r * len + len - 1] * channels + c, acc);
+      join_store<V>(acc, scale, table + (int64_t)keys[r * len + len - 1] * channels + c);
     }
     __syncthreads();
   }
