@@ -471,8 +471,10 @@ EmbedPlan embed_plan(const so2conv_embed_desc *d, int64_t n, int which) {
     p.passes = (bits + 7) / 8;
     p.bits = (bits + p.passes - 1) / p.passes;
     p.nb = (int)ceil_div(n, SORT_TILE);
-    // about 32 warps of ranges for each SM
-    p.len = (int)(ceil_div(ceil_div(n, MODEL_SMS * 32), RUN_ROWS) * RUN_ROWS);
+    // about 16 warps of ranges for each SM, which keep eight rows each in
+    // flight; with 32 the runs took as long and their join 10 us more of 130
+    // (a million tokens of 100 elements, 128 channels)
+    p.len = (int)(ceil_div(ceil_div(n, MODEL_SMS * 16), RUN_ROWS) * RUN_ROWS);
     if (p.len < 2 * RUN_ROWS) p.len = 2 * RUN_ROWS;
     p.n_ranges = ceil_div(n, p.len);
     for (int i = 0; i < 2; ++i) {

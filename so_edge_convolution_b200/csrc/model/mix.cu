@@ -116,30 +116,66 @@ __global__ void __launch_bounds__(ROWS_THREADS)
 }
 
 // ---- forward, by index -------------------------------------------------------------
+// A thread owns V columns and takes the systems of its blockIdx.y one after
+// the other, four slots' rows in flight; the slots' experts and weights lie in
+// shared memory, unused ones as expert -1.
+constexpr int SLOT_STAGE = 1024;  // slots staged together
+
 template <int V, typename TE, typename TO>
-__global__ void k_mix(int64_t n_systems, int K, int top_k, int64_t n, const TE *__restrict__ experts,
-                      const float *__restrict__ weights, const int *__restrict__ index,
-                      TO *__restrict__ out, DevStatus *st) {
-  const int64_t c = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) * V;
-  if (c >= n) return;
-  for (int64_t t = blockIdx.y; t < n_systems; t += gridDim.y) {
-    float acc[V];
+__global__ void __launch_bounds__(256)
+    k_mix(int n_systems, int K, int top_k, int64_t n, const TE *__restrict__ experts,
+          const float *__restrict__ weights, const int *__restrict__ index, TO *__restrict__ out,
+          DevStatus *st) {
+  __shared__ int se[SLOT_STAGE];
+  __shared__ float sw[SLOT_STAGE];
+  const int64_t c = (blockIdx.x * 256ll + threadIdx.x) * V;
+  const int per = (n_systems + gridDim.y - 1) / gridDim.y;
+  const int ta = blockIdx.y * per, tb = ta + per < n_systems ? ta + per : n_systems;
+  const int64_t p0 = (int64_t)ta * top_k, slots = (int64_t)(tb - ta) * top_k;
+  const TE *col = experts + c;
+  int t = ta, j = 0;  // of the next slot
+  float acc[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    for (int j = 0; j < top_k; ++j) {
-      const int64_t p = t * top_k + j;
-      const int e = index[p];
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int64_t q0 = 0; q0 < slots; q0 += SLOT_STAGE) {
+    const int have = slots - q0 < SLOT_STAGE ? (int)(slots - q0) : SLOT_STAGE;
+    __syncthreads();
+    for (int i = threadIdx.x; i < have; i += 256) {
+      const int64_t p = p0 + q0 + i;
+      int e = index[p];
       if (e < 0 || e >= K) {
-        if (e != -1 && c == 0) raise_error(st, SO2_ERR_INDEX, (int)p);
-        continue;
+        if (e != -1 && blockIdx.x == 0) raise_error(st, SO2_ERR_INDEX, (int)p);
+        e = -1;
       }
-      const float w = weights[p];
-      float x[V];
-      load_vec<V>(experts + e * n + c, x);
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = fmaf(w, x[v], acc[v]);
+      se[i] = e;
+      sw[i] = e >= 0 ? weights[p] : 0.f;
     }
-    store_vec<V>(out + t * n + c, acc);
+    __syncthreads();
+    if (c >= n) continue;
+    for (int i = 0; i < have; i += 4) {
+      float x[4][V];
+      int e[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        e[u] = i + u < have ? se[i + u] : -1;
+        if (e[u] >= 0) load_vec<V>(col + e[u] * n, x[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (i + u >= have) break;
+        if (e[u] >= 0) {
+          const float w = sw[i + u];
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] = fmaf(w, x[u][v], acc[v]);
+        }
+        if (++j == top_k) {
+          store_vec<V>(out + t * n + c, acc);
+          j = 0, ++t;
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] = 0.f;
+        }
+      }
+    }
   }
 }
 
@@ -172,25 +208,49 @@ __global__ void k_mix_lists(int n_slots, int K, const int *__restrict__ index,
   }
 }
 
+// A thread owns V columns and the experts of its blockIdx.y; the expert's
+// slots four at a time.  Lists of up to SLOT_STAGE slots are read from shared
+// memory, longer ones from where they are.
 template <int V>
-__global__ void k_mix_grad_experts(int64_t n_systems, int K, int top_k, int64_t n,
-                                   const float *__restrict__ weights,
-                                   const int *__restrict__ offsets, const int *__restrict__ list,
-                                   const float *__restrict__ grad, float *__restrict__ ge) {
-  const int64_t c = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) * V;
+__global__ void __launch_bounds__(256)
+    k_mix_grad_experts(int n_slots, int K, int top_k, int64_t n, const float *__restrict__ weights,
+                       const int *__restrict__ offsets, const int *__restrict__ list,
+                       const float *__restrict__ grad, float *__restrict__ ge) {
+  __shared__ int st[SLOT_STAGE];
+  __shared__ float sw[SLOT_STAGE];
+  const int per = (K + gridDim.y - 1) / gridDim.y;
+  const int ea = blockIdx.y * per, eb = ea + per < K ? ea + per : K;
+  const int first = ea < eb ? offsets[ea] : 0, end = ea < eb ? offsets[eb] : 0;
+  const bool staged = end - first <= SLOT_STAGE;
+  if (staged)
+    for (int i = first + threadIdx.x; i < end; i += 256) {
+      const int p = list[i];
+      st[i - first] = p / top_k;
+      sw[i - first] = weights[p];
+    }
+  __syncthreads();
+  const int64_t c = (blockIdx.x * 256ll + threadIdx.x) * V;
   if (c >= n) return;
-  for (int e = blockIdx.y; e < K; e += gridDim.y) {
+  for (int e = ea; e < eb; ++e) {
     const int a = offsets[e], b = offsets[e + 1];
     float acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    for (int q = a; q < b; ++q) {
-      const int p = list[q];
-      const float w = weights[p];
-      float g[V];
-      load_vec<V>(grad + (int64_t)(p / top_k) * n + c, g);
+    for (int q = a; q < b; q += 4) {
+      float g[4][V], w[4];
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = fmaf(w, g[v], acc[v]);
+      for (int u = 0; u < 4; ++u) {
+        if (q + u >= b) break;
+        const int t = staged ? st[q + u - first] : list[q + u] / top_k;
+        w[u] = staged ? sw[q + u - first] : weights[list[q + u]];
+        load_vec<V>(grad + t * n + c, g[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (q + u >= b) break;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(w[u], g[u][v], acc[v]);
+      }
     }
     store_vec<V>(ge + e * n + c, acc);
   }
@@ -316,37 +376,53 @@ __global__ void __launch_bounds__(256, 2)
   }
 }
 
-// One slot a warp over the block's share of the columns: part[split][slot].
+// Four slots of one system a warp over the block's share of the columns, which
+// read the system's gradient once: part[split][slot].
 template <int V, typename TE>
-__global__ void k_mix_dot_slots(int64_t n_slots, int K, int top_k, int64_t n,
-                                const TE *__restrict__ experts, const int *__restrict__ index,
-                                const float *__restrict__ grad, float *__restrict__ part) {
+__global__ void __launch_bounds__(256)
+    k_mix_dot_slots(int n_systems, int K, int top_k, int64_t n, const TE *__restrict__ experts,
+                    const int *__restrict__ index, const float *__restrict__ grad,
+                    float *__restrict__ part) {
   const int lane = threadIdx.x & 31;
   const int64_t len = ((n + gridDim.x - 1) / gridDim.x + V - 1) / V * V;
   const int64_t c0 = blockIdx.x * len, c1 = c0 + len < n ? c0 + len : n;
-  for (int64_t p = blockIdx.y * 8 + (threadIdx.x >> 5); p < n_slots; p += gridDim.y * 8) {
-    const int e = index[p];
-    float s[V];
+  const int quads = (top_k + 3) / 4;
+  const int64_t jobs = (int64_t)n_systems * quads, n_slots = (int64_t)n_systems * top_k;
+  for (int64_t job = blockIdx.y * 8 + (threadIdx.x >> 5); job < jobs; job += gridDim.y * 8) {
+    const int64_t t = job / quads;
+    const int j0 = (int)(job - t * quads) * 4;
+    const float *g = grad + t * n;
+    const TE *x[4];
+    float s[4][V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = 0.f;
-    if (e >= 0 && e < K) {
-      const TE *x = experts + e * n;
-      const float *g = grad + (p / top_k) * n;
-#pragma unroll 4
-      for (int64_t c = c0 + lane * V; c < c1; c += 32 * V) {
-        float a[V], b[V];
-        load_vec<V>(x + c, a);
-        load_vec<V>(g + c, b);
+    for (int u = 0; u < 4; ++u) {
+      const int e = j0 + u < top_k ? index[t * top_k + j0 + u] : -1;
+      x[u] = e >= 0 && e < K ? experts + e * n : nullptr;
 #pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = fmaf(a[v], b[v], s[v]);
-      }
+      for (int v = 0; v < V; ++v) s[u][v] = 0.f;
     }
-    float sum = s[0];
+#pragma unroll 2
+    for (int64_t c = c0 + lane * V; c < c1; c += 32 * V) {
+      float b[V], a[4][V];
+      load_vec<V>(g + c, b);
 #pragma unroll
-    for (int v = 1; v < V; ++v) sum += s[v];
+      for (int u = 0; u < 4; ++u)
+        if (x[u]) load_vec<V>(x[u] + c, a[u]);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) part[blockIdx.x * n_slots + p] = sum;
+      for (int u = 0; u < 4; ++u)
+        if (x[u])
+#pragma unroll
+          for (int v = 0; v < V; ++v) s[u][v] = fmaf(a[u][v], b[v], s[u][v]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float sum = s[u][0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) sum += s[u][v];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0 && j0 + u < top_k) part[blockIdx.x * n_slots + t * top_k + j0 + u] = sum;
+    }
   }
 }
 
@@ -465,10 +541,13 @@ void launch_mix(const so2conv_mix_desc *d, int64_t n_systems, const void *expert
                    static_cast<const TE *>(experts), static_cast<TO *>(out), s);
     return;
   }
-  const dim3 grid((unsigned)ceil_div(d->n_weights, 256 * V), (unsigned)(n_systems < 4 ? n_systems : 4));
-  k_mix<V, TE, TO><<<grid, 256, 0, s>>>(n_systems, d->n_experts, d->top_k, d->n_weights,
-                                        static_cast<const TE *>(experts), weights, index,
-                                        static_cast<TO *>(out), st);
+  // about four resident blocks an SM
+  const int64_t cols = ceil_div(d->n_weights, 256 * V);
+  int64_t rows = ceil_div(MODEL_SMS * 4, cols);
+  if (rows > n_systems) rows = n_systems;
+  k_mix<V, TE, TO><<<dim3((unsigned)cols, (unsigned)rows), 256, 0, s>>>(
+      (int)n_systems, d->n_experts, d->top_k, d->n_weights, static_cast<const TE *>(experts),
+      weights, index, static_cast<TO *>(out), st);
 }
 
 template <typename TE, typename TO>
@@ -486,7 +565,6 @@ so2_status mix_dots(const so2conv_mix_desc *d, int64_t n_systems, const MixPlan 
                     const void *experts, const int32_t *index, const float *grad, float *part,
                     cudaStream_t s) {
   const TE *x = static_cast<const TE *>(experts);
-  const int64_t slots = n_systems * d->top_k;
   if (p.tiles) {
     constexpr int red = 4 * DOT_T * DOT_E * 4;
     constexpr int smem = DOT_STAGES * dot_stage_bytes<TE>() > red ? DOT_STAGES * dot_stage_bytes<TE>() : red;
@@ -496,9 +574,9 @@ so2_status mix_dots(const so2conv_mix_desc *d, int64_t n_systems, const MixPlan 
     k_mix_dot_tiles<VEC, TE><<<dim3(p.splits, (unsigned)tiles), 256, smem, s>>>(
         (int)n_systems, d->n_experts, d->n_weights, x, grad, part);
   } else {
-    const int64_t rows = ceil_div(slots, 8);
-    k_mix_dot_slots<VEC ? 4 : 1, TE><<<dim3(p.splits, (unsigned)(rows < 16 ? rows : 16)), 256, 0, s>>>(
-        slots, d->n_experts, d->top_k, d->n_weights, x, index, grad, part);
+    const int64_t rows = ceil_div(n_systems * ceil_div(d->top_k, 4), 8);
+    k_mix_dot_slots<VEC ? 4 : 1, TE><<<dim3(p.splits, (unsigned)(rows < 65535 ? rows : 65535)), 256, 0, s>>>(
+        (int)n_systems, d->n_experts, d->top_k, d->n_weights, x, index, grad, part);
   }
   MODEL_CKL();
   return SO2_OK;
@@ -574,16 +652,19 @@ so2_status so2conv_mix_experts_backward(const so2conv_mix_desc *d, int64_t n_sys
   const bool vec = n % 4 == 0 && aligned_to(experts, 4 * es) && aligned_to(grad_out, 16) &&
                    aligned_to(grad_experts, 16);
   if (grad_experts) {
-    const dim3 grid((unsigned)ceil_div(n, vec ? 1024 : 256), (unsigned)(K < 4 ? K : 4));
+    const int64_t cols = ceil_div(n, vec ? 1024 : 256);
+    int64_t rows = ceil_div(MODEL_SMS * 8, cols);
+    if (rows > K) rows = K;
+    const dim3 grid((unsigned)cols, (unsigned)rows);
     if (!index && vec)
       launch_rows<4>(K, (int)n_systems, n, weights, 1, k, grad_out, grad_experts, s);
     else if (!index)
       launch_rows<1>(K, (int)n_systems, n, weights, 1, k, grad_out, grad_experts, s);
     else if (vec)
-      k_mix_grad_experts<4><<<grid, 256, 0, s>>>(n_systems, K, k, n, weights, offsets, list,
+      k_mix_grad_experts<4><<<grid, 256, 0, s>>>((int)slots, K, k, n, weights, offsets, list,
                                                  grad_out, grad_experts);
     else
-      k_mix_grad_experts<1><<<grid, 256, 0, s>>>(n_systems, K, k, n, weights, offsets, list,
+      k_mix_grad_experts<1><<<grid, 256, 0, s>>>((int)slots, K, k, n, weights, offsets, list,
                                                  grad_out, grad_experts);
     MODEL_CKL();
   }
