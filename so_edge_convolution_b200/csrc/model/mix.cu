@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(ROWS_THREADS)
 // A thread owns V columns and takes the systems of its blockIdx.y one after
 // the other, four slots' rows in flight; the slots' experts and weights lie in
 // shared memory, unused ones as expert -1.
-constexpr int SLOT_STAGE = 1024;  // slots staged together
+constexpr int SLOT_STAGE = 4096;  // slots staged together: all of a system's at least
 
 template <int V, typename TE, typename TO>
 __global__ void __launch_bounds__(256)
@@ -131,17 +131,13 @@ __global__ void __launch_bounds__(256)
   const int64_t c = (blockIdx.x * 256ll + threadIdx.x) * V;
   const int per = (n_systems + gridDim.y - 1) / gridDim.y;
   const int ta = blockIdx.y * per, tb = ta + per < n_systems ? ta + per : n_systems;
-  const int64_t p0 = (int64_t)ta * top_k, slots = (int64_t)(tb - ta) * top_k;
+  const int together = SLOT_STAGE / top_k;
   const TE *col = experts + c;
-  int t = ta, j = 0;  // of the next slot
-  float acc[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.f;
-  for (int64_t q0 = 0; q0 < slots; q0 += SLOT_STAGE) {
-    const int have = slots - q0 < SLOT_STAGE ? (int)(slots - q0) : SLOT_STAGE;
+  for (int t0 = ta; t0 < tb; t0 += together) {
+    const int t1 = t0 + together < tb ? t0 + together : tb;
     __syncthreads();
-    for (int i = threadIdx.x; i < have; i += 256) {
-      const int64_t p = p0 + q0 + i;
+    for (int i = threadIdx.x; i < (t1 - t0) * top_k; i += 256) {
+      const int64_t p = (int64_t)t0 * top_k + i;
       int e = index[p];
       if (e < 0 || e >= K) {
         if (e != -1 && blockIdx.x == 0) raise_error(st, SO2_ERR_INDEX, (int)p);
@@ -152,29 +148,28 @@ __global__ void __launch_bounds__(256)
     }
     __syncthreads();
     if (c >= n) continue;
-    for (int i = 0; i < have; i += 4) {
-      float x[4][V];
-      int e[4];
+    for (int t = t0; t < t1; ++t) {
+      float acc[V];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        e[u] = i + u < have ? se[i + u] : -1;
-        if (e[u] >= 0) load_vec<V>(col + e[u] * n, x[u]);
-      }
+      for (int v = 0; v < V; ++v) acc[v] = 0.f;
+      const int i0 = (t - t0) * top_k;
+      for (int j = 0; j < top_k; j += 4) {
+        float x[4][V];
+        int e[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (i + u >= have) break;
-        if (e[u] >= 0) {
-          const float w = sw[i + u];
-#pragma unroll
-          for (int v = 0; v < V; ++v) acc[v] = fmaf(w, x[u][v], acc[v]);
+        for (int u = 0; u < 4; ++u) {
+          e[u] = j + u < top_k ? se[i0 + j + u] : -1;
+          if (e[u] >= 0) load_vec<V>(col + e[u] * n, x[u]);
         }
-        if (++j == top_k) {
-          store_vec<V>(out + t * n + c, acc);
-          j = 0, ++t;
 #pragma unroll
-          for (int v = 0; v < V; ++v) acc[v] = 0.f;
-        }
+        for (int u = 0; u < 4; ++u)
+          if (e[u] >= 0) {
+            const float w = sw[i0 + j + u];
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] = fmaf(w, x[u][v], acc[v]);
+          }
       }
+      store_vec<V>(out + t * n + c, acc);
     }
   }
 }
@@ -426,22 +421,137 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// gw[slot] from the splits: of all (t, e) (all) or of the slots.  One warp a slot.
-__global__ void k_mix_dots_join(int64_t n_slots, int K, int top_k, const int *__restrict__ index,
-                                bool all, int64_t stride, int splits,
-                                const float *__restrict__ part, float *__restrict__ gw) {
-  const int lane = threadIdx.x & 31;
-  const int64_t p = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (p >= n_slots) return;
-  const int e = index ? index[p] : (int)(p % top_k);
-  float s = 0.f;
-  if (e >= 0 && e < K) {
-    const int64_t at = all ? (p / top_k) * K + e : p;
-    for (int i = lane; i < splits; i += 32) s += part[i * stride + at];
+// Both gradients by index, for the systems whose gradients fit a block's shared
+// memory: a block stages `cols` columns of all of them with asynchronous
+// copies, forms the experts' gradient there from groups of cols / 4 threads
+// (four columns a thread, an expert a group) and the slots' products from its
+// warps.  grad_out is read once and nothing else passes through L2 twice but
+// the experts' rows that several systems name.  part[tile][slot].
+constexpr int BACK_SLOTS = 2048, BACK_EXPERTS = 1024, BACK_BYTES = 96 * 1024;
+
+template <int COLS, typename TE>
+__global__ void __launch_bounds__(256)
+    k_mix_back_slots(int T, int K, int top_k, int64_t n, const TE *__restrict__ experts,
+                     const float *__restrict__ weights, const int *__restrict__ index,
+                     const int *__restrict__ offsets, const int *__restrict__ list,
+                     const float *__restrict__ grad, float *__restrict__ ge,
+                     float *__restrict__ part) {
+  extern __shared__ __align__(16) unsigned char sm[];
+  const int slots = T * top_k, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  float *stage = reinterpret_cast<float *>(sm);  // [2][T][COLS]
+  int2 *by_expert = reinterpret_cast<int2 *>(stage + 2 * T * COLS);  // the lists: system's place, weight
+  int2 *by_slot = by_expert + slots;                                 // the slots: place, expert or -1
+  int *off = reinterpret_cast<int *>(by_slot + slots);               // [K + 1]
+  const int64_t tiles = (n + COLS - 1) / COLS;
+  auto load = [&](int64_t tile) {
+    if (tile < tiles) {
+      constexpr int VECS = COLS / 4, STEP = 256 / VECS;
+      const int c = (tid % VECS) * 4;
+      const int64_t at = tile * COLS + c;
+      float *g = stage + (tile / gridDim.x & 1) * T * COLS;
+      for (int t = tid / VECS; t < T; t += STEP)
+        copy_async_or_zero<16>(g + t * COLS + c, grad + t * n + (at < n ? at : 0), at < n);
+    }
+    copy_commit();
+  };
+  load(blockIdx.x);
+  const int named = offsets[K];
+  for (int i = tid; i < slots; i += 256) {
+    if (i < named) {
+      const int p = list[i];
+      by_expert[i] = make_int2(p / top_k * COLS, __float_as_int(weights[p]));
+    }
+    const int e = index[i];
+    by_slot[i] = make_int2(i / top_k * COLS, e >= 0 && e < K ? e : -1);
   }
+  for (int i = tid; i <= K; i += 256) off[i] = offsets[i];
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    load(tile + gridDim.x);  // into the buffer that the last step is done with
+    copy_wait<1>();
+    __syncthreads();
+    const float *g = stage + (tile / gridDim.x & 1) * T * COLS;
+    const int64_t c0 = tile * COLS;
+    const int have = n - c0 < COLS ? (int)(n - c0) : COLS;  // a multiple of four
+    if (ge) {
+      constexpr int GROUP = COLS / 4;
+      const int c = (tid % GROUP) * 4;
+      float *to = ge + c0 + c;
+      for (int e = tid / GROUP; e < K; e += 256 / GROUP) {
+        float acc[4] = {};
+        const int b = off[e + 1];
+        for (int q = off[e]; q < b; ++q) {
+          const int2 slot = by_expert[q];
+          float x[4];
+          load_vec<4>(g + slot.x + c, x);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[v] = fmaf(__int_as_float(slot.y), x[v], acc[v]);
+        }
+        if (c < have) store_vec<4>(to + e * n, acc);
+      }
+    }
+    if (part) {
+      // S slots a warp and step, all their vectors in flight
+      constexpr int H = COLS / 128, S = H >= 4 ? 2 : 4;
+      for (int p = w; p < slots; p += 8 * S) {
+        int2 slot[S];
+        float x[S][H][4], sum[S];
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+          slot[u] = p + 8 * u < slots ? by_slot[p + 8 * u] : make_int2(0, -1);
+          sum[u] = 0.f;
+          const TE *from = experts + slot[u].y * n + c0 + lane * 4;
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            if (slot[u].y >= 0 && h * 128 + lane * 4 < have) load_vec<4>(from + h * 128, x[u][h]);
+        }
+#pragma unroll
+        for (int u = 0; u < S; ++u)
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            if (slot[u].y >= 0 && h * 128 + lane * 4 < have) {
+              float y[4];
+              load_vec<4>(g + slot[u].x + h * 128 + lane * 4, y);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) sum[u] = fmaf(x[u][h][v], y[v], sum[u]);
+            }
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+#pragma unroll
+          for (int o = 16; o; o >>= 1) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
+          if (lane == 0 && p + 8 * u < slots) part[tile * slots + p + 8 * u] = sum[u];
+        }
+      }
+    }
+    __syncthreads();  // everyone is done with this buffer
+  }
+  copy_wait<0>();
+}
+
+// gw[slot] from the splits: of all (t, e) (all) or of the slots.  A lane a
+// slot, so that the partial sums are read side by side; a warp takes every
+// 32nd split, and the warps' sums are added in a tree.
+__global__ void __launch_bounds__(1024)
+    k_mix_dots_join(int64_t n_slots, int K, int top_k, const int *__restrict__ index, bool all,
+                    int64_t stride, int splits, const float *__restrict__ part,
+                    float *__restrict__ gw) {
+  __shared__ float sums[32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t p = blockIdx.x * 32ll + lane;
+  float s = 0.f;
+  if (p < n_slots) {
+    const int e = index ? index[p] : (int)(p % top_k);
+    if (e >= 0 && e < K) {
+      const int64_t at = all ? (p / top_k) * K + e : p;
+#pragma unroll 8
+      for (int i = w; i < splits; i += 32) s += part[i * stride + at];
+    }
+  }
+  sums[w][lane] = s;
+  __syncthreads();
+  s = sums[lane][w];  // of slot w, from warp `lane`
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) gw[p] = s;
+  if (lane == 0 && blockIdx.x * 32ll + w < n_slots) gw[blockIdx.x * 32ll + w] = s;
 }
 
 }  // namespace so2
@@ -453,6 +563,7 @@ namespace {
 struct MixPlan {
   size_t status, offsets, list, part, total;
   bool tiles;  // the products of all (t, e), or of the slots alone
+  int cols;    // both gradients by index together: a block's columns, or 0
   int splits;
 };
 
@@ -480,6 +591,16 @@ MixPlan mix_plan(const so2conv_mix_desc *d, int64_t n_systems, int which) {
     p.tiles = d->top_k * 8 >= d->n_experts;
     const int64_t per = p.tiles ? n_systems * d->n_experts : n_systems * d->top_k;  // products
     int64_t want;
+    // All systems' gradients of at least 128 columns in a block's shared memory
+    // (two blocks an SM): 33 systems, top 4 of 64, 307,200 weights take 30 us
+    // for both gradients where the separate kernels take 58.
+    p.cols = 0;
+    if (!p.tiles && n_systems > 0 && slots <= BACK_SLOTS && d->n_experts <= BACK_EXPERTS &&
+        d->n_weights % 4 == 0) {
+      p.cols = 512;
+      while (p.cols >= 128 && n_systems * p.cols * 8 > BACK_BYTES) p.cols /= 2;
+      if (p.cols < 128) p.cols = 0;
+    }
     if (p.tiles) {  // two resident blocks an SM
       const int64_t t = ceil_div(n_systems, DOT_T) * ceil_div(d->n_experts, DOT_E);
       want = ceil_div(2 * MODEL_SMS, t > 0 ? t : 1);
@@ -490,6 +611,8 @@ MixPlan mix_plan(const so2conv_mix_desc *d, int64_t n_systems, int which) {
     // at most 16 M partial sums
     const int64_t most = per > 0 ? (16ll << 20) / per : 1;
     p.splits = (int)(want < most ? want : (most > 0 ? most : 1));
+    // (a block a column range; the partial sums are a part in `cols` of the operands)
+    if (p.cols) p.splits = (int)ceil_div(d->n_weights, p.cols);
     p.part = ws_take(c, sizeof(float) * (size_t)(per * p.splits));
   }
   p.total = (c + 255) & ~static_cast<size_t>(255);
@@ -536,14 +659,15 @@ template <int V, typename TE, typename TO>
 void launch_mix(const so2conv_mix_desc *d, int64_t n_systems, const void *experts,
                 const float *weights, const int32_t *index, void *out, DevStatus *st,
                 cudaStream_t s) {
-  if (!index) {
-    launch_rows<V>((int)n_systems, d->n_experts, d->n_weights, weights, d->top_k, 1,
-                   static_cast<const TE *>(experts), static_cast<TO *>(out), s);
-    return;
+  if constexpr (V <= 4) {
+    if (!index) {
+      launch_rows<V>((int)n_systems, d->n_experts, d->n_weights, weights, d->top_k, 1,
+                     static_cast<const TE *>(experts), static_cast<TO *>(out), s);
+      return;
+    }
   }
-  // about four resident blocks an SM
   const int64_t cols = ceil_div(d->n_weights, 256 * V);
-  int64_t rows = ceil_div(MODEL_SMS * 4, cols);
+  int64_t rows = ceil_div(MODEL_SMS * 16, cols);
   if (rows > n_systems) rows = n_systems;
   k_mix<V, TE, TO><<<dim3((unsigned)cols, (unsigned)rows), 256, 0, s>>>(
       (int)n_systems, d->n_experts, d->top_k, d->n_weights, static_cast<const TE *>(experts),
@@ -554,10 +678,47 @@ template <typename TE, typename TO>
 void launch_mix(bool vec, const so2conv_mix_desc *d, int64_t n_systems, const void *experts,
                 const float *weights, const int32_t *index, void *out, DevStatus *st,
                 cudaStream_t s) {
-  if (vec)
+  // by index, eight columns a thread where both sides allow it: half the
+  // instructions a column of four
+  if (vec && index && d->n_weights % 8 == 0 && aligned_to(experts, 16) && aligned_to(out, 16))
+    launch_mix<8, TE, TO>(d, n_systems, experts, weights, index, out, st, s);
+  else if (vec)
     launch_mix<4, TE, TO>(d, n_systems, experts, weights, index, out, st, s);
   else
     launch_mix<1, TE, TO>(d, n_systems, experts, weights, index, out, st, s);
+}
+
+template <int COLS, typename TE>
+so2_status mix_back_slots(const so2conv_mix_desc *d, int64_t T, const MixPlan &p, const TE *experts,
+                          const float *weights, const int32_t *index, const int *offsets,
+                          const int *list, const float *grad, float *ge, float *part,
+                          cudaStream_t s) {
+  const size_t smem = (size_t)T * COLS * 8 + T * d->top_k * 16 + (d->n_experts + 1) * 4;
+  MODEL_CK(cudaFuncSetAttribute(k_mix_back_slots<COLS, TE>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  // as many blocks as stay resident, which then take equal shares of the tiles
+  int fit = (int)(224 * 1024 / (smem + 1024));
+  if (fit > 4) fit = 4;
+  const int64_t steps = ceil_div(p.splits, MODEL_SMS * fit);
+  const unsigned grid = (unsigned)ceil_div(p.splits, steps);
+  k_mix_back_slots<COLS, TE><<<grid, 256, smem, s>>>((int)T, d->n_experts, d->top_k, d->n_weights,
+                                                         experts, weights, index, offsets, list, grad,
+                                                         ge, part);
+  MODEL_CKL();
+  return SO2_OK;
+}
+
+template <typename TE>
+so2_status mix_back_slots(const so2conv_mix_desc *d, int64_t T, const MixPlan &p,
+                          const void *experts, const float *weights, const int32_t *index,
+                          const int *offsets, const int *list, const float *grad, float *ge,
+                          float *part, cudaStream_t s) {
+  const TE *x = static_cast<const TE *>(experts);
+  if (p.cols == 512)
+    return mix_back_slots<512, TE>(d, T, p, x, weights, index, offsets, list, grad, ge, part, s);
+  if (p.cols == 256)
+    return mix_back_slots<256, TE>(d, T, p, x, weights, index, offsets, list, grad, ge, part, s);
+  return mix_back_slots<128, TE>(d, T, p, x, weights, index, offsets, list, grad, ge, part, s);
 }
 
 template <bool VEC, typename TE>
@@ -651,6 +812,22 @@ so2_status so2conv_mix_experts_backward(const so2conv_mix_desc *d, int64_t n_sys
   const size_t es = dtype_size(d->expert_dtype);
   const bool vec = n % 4 == 0 && aligned_to(experts, 4 * es) && aligned_to(grad_out, 16) &&
                    aligned_to(grad_experts, 16);
+  if (vec && p.cols) {
+    if (!grad_experts && !grad_weights) return SO2_OK;
+    float *part = grad_weights ? ws_at<float>(ws, p.part) : nullptr;
+    r = d->expert_dtype == SO2_F32
+            ? mix_back_slots<float>(d, n_systems, p, experts, weights, index, offsets, list, grad_out,
+                                    grad_experts, part, s)
+            : mix_back_slots<__nv_bfloat16>(d, n_systems, p, experts, weights, index, offsets, list,
+                                            grad_out, grad_experts, part, s);
+    if (r != SO2_OK) return r;
+    if (grad_weights) {
+      k_mix_dots_join<<<(unsigned)ceil_div(slots, 32), 1024, 0, s>>>(
+          slots, K, k, index, false, slots, p.splits, part, grad_weights);
+      MODEL_CKL();
+    }
+    return SO2_OK;
+  }
   if (grad_experts) {
     const int64_t cols = ceil_div(n, vec ? 1024 : 256);
     int64_t rows = ceil_div(MODEL_SMS * 8, cols);
@@ -679,7 +856,7 @@ so2_status so2conv_mix_experts_backward(const so2conv_mix_desc *d, int64_t n_sys
       r2 = vec ? mix_dots<true, bf>(d, n_systems, p, experts, index, grad_out, part, s)
                : mix_dots<false, bf>(d, n_systems, p, experts, index, grad_out, part, s);
     if (r2 != SO2_OK) return r2;
-    k_mix_dots_join<<<(unsigned)ceil_div(slots, 8), 256, 0, s>>>(
+    k_mix_dots_join<<<(unsigned)ceil_div(slots, 32), 1024, 0, s>>>(
         slots, K, k, index, p.tiles, p.tiles ? n_systems * K : slots, p.splits, part, grad_weights);
     MODEL_CKL();
   }
