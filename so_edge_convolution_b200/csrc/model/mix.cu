@@ -3,7 +3,7 @@
 // The slots (t, j) that name an expert form its list, in slot order; a small
 // kernel builds the lists once per backward call.  With every expert in order
 // (no index) slot (t, e) names expert e, and no lists are needed.
-#include "model_common.cuh"
+#include "mix_tc.cuh"
 
 namespace so2 {
 
@@ -17,6 +17,9 @@ namespace so2 {
 constexpr int ROWS_THREADS = 128;
 constexpr int ROWS_SC = 32;     // rows of B whose weights are staged together
 constexpr int ROWS_DEPTH = 8;   // copies in flight
+// From R S / (R + S) on (the FMAs over the bytes) the tensor cores take the
+// product (mix_tc.cuh).
+constexpr int MIX_TC_FROM = 10;
 
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
@@ -639,8 +642,8 @@ so2_status mix_checks(const so2conv_mix_desc *d, int64_t n_systems, const void *
 // Rows of C a thread holds: all of them up to 32, else the fewest passes over B
 // with evenly filled ones.
 template <int V, typename TB, typename TC>
-void launch_rows(int R, int S, int64_t n, const float *M, int64_t mr, int64_t ms, const TB *B, TC *C,
-                 cudaStream_t s) {
+so2_status launch_rows_fma(int R, int S, int64_t n, const float *M, int64_t mr, int64_t ms,
+                           const TB *B, TC *C, cudaStream_t s) {
   const unsigned grid = (unsigned)ceil_div(n, ROWS_THREADS * V);
   const int passes = (R + 31) / 32, tt = (R + passes - 1) / passes;
 #define MIX_ROWS(TT) \
@@ -653,18 +656,53 @@ void launch_rows(int R, int S, int64_t n, const float *M, int64_t mr, int64_t ms
   else if (tt <= 24) MIX_ROWS(24);
   else MIX_ROWS(32);
 #undef MIX_ROWS
+  MODEL_CKL();
+  return SO2_OK;
+}
+
+template <int N, int KB, typename TB, typename TC>
+so2_status launch_rows_tc(int r0, int R, int S, int64_t n, const float *M, int64_t mr, int64_t ms,
+                          const TB *B, TC *C, DevStatus *st, cudaStream_t s) {
+  const int blocks = (S + KB - 1) / KB, smem = mixtc_smem<TB>(KB, blocks);
+  MODEL_CK(cudaFuncSetAttribute(k_mix_tc<N, KB, TB, TC>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  const int64_t tiles = ceil_div(n, MIXTC_COLS);
+  const int64_t most = MODEL_SMS * (smem <= 110 * 1024 ? 2 : 1);
+  k_mix_tc<N, KB, TB, TC><<<(unsigned)(tiles < most ? tiles : most), MIXTC_THREADS, smem, s>>>(
+      r0, R, S, blocks, n, M, mr, ms, B, C, st);
+  MODEL_CKL();
+  return SO2_OK;
+}
+
+template <int V, typename TB, typename TC>
+so2_status launch_rows(int R, int S, int64_t n, const float *M, int64_t mr, int64_t ms, const TB *B,
+                       TC *C, DevStatus *st, cudaStream_t s) {
+  if constexpr (V == 4) {
+    if (S <= MIXTC_MAX_S && (int64_t)R * S >= MIX_TC_FROM * (R + S)) {
+      for (int r0 = 0; r0 < R; r0 += MIXTC_ROWS) {
+        so2_status e;
+        if (R - r0 <= 32)
+          e = S <= 32 ? launch_rows_tc<32, 32>(r0, R, S, n, M, mr, ms, B, C, st, s)
+                      : launch_rows_tc<32, 64>(r0, R, S, n, M, mr, ms, B, C, st, s);
+        else
+          e = S <= 32 ? launch_rows_tc<64, 32>(r0, R, S, n, M, mr, ms, B, C, st, s)
+                      : launch_rows_tc<64, 64>(r0, R, S, n, M, mr, ms, B, C, st, s);
+        if (e != SO2_OK) return e;
+      }
+      return SO2_OK;
+    }
+  }
+  return launch_rows_fma<V>(R, S, n, M, mr, ms, B, C, s);
 }
 
 template <int V, typename TE, typename TO>
-void launch_mix(const so2conv_mix_desc *d, int64_t n_systems, const void *experts,
+so2_status launch_mix(const so2conv_mix_desc *d, int64_t n_systems, const void *experts,
                 const float *weights, const int32_t *index, void *out, DevStatus *st,
                 cudaStream_t s) {
   if constexpr (V <= 4) {
-    if (!index) {
-      launch_rows<V>((int)n_systems, d->n_experts, d->n_weights, weights, d->top_k, 1,
-                     static_cast<const TE *>(experts), static_cast<TO *>(out), s);
-      return;
-    }
+    if (!index)
+      return launch_rows<V>((int)n_systems, d->n_experts, d->n_weights, weights, d->top_k, 1,
+                            static_cast<const TE *>(experts), static_cast<TO *>(out), st, s);
   }
   const int64_t cols = ceil_div(d->n_weights, 256 * V);
   int64_t rows = ceil_div(MODEL_SMS * 16, cols);
@@ -672,20 +710,20 @@ void launch_mix(const so2conv_mix_desc *d, int64_t n_systems, const void *expert
   k_mix<V, TE, TO><<<dim3((unsigned)cols, (unsigned)rows), 256, 0, s>>>(
       (int)n_systems, d->n_experts, d->top_k, d->n_weights, static_cast<const TE *>(experts),
       weights, index, static_cast<TO *>(out), st);
+  MODEL_CKL();
+  return SO2_OK;
 }
 
 template <typename TE, typename TO>
-void launch_mix(bool vec, const so2conv_mix_desc *d, int64_t n_systems, const void *experts,
+so2_status launch_mix(bool vec, const so2conv_mix_desc *d, int64_t n_systems, const void *experts,
                 const float *weights, const int32_t *index, void *out, DevStatus *st,
                 cudaStream_t s) {
   // by index, eight columns a thread where both sides allow it: half the
   // instructions a column of four
   if (vec && index && d->n_weights % 8 == 0 && aligned_to(experts, 16) && aligned_to(out, 16))
-    launch_mix<8, TE, TO>(d, n_systems, experts, weights, index, out, st, s);
-  else if (vec)
-    launch_mix<4, TE, TO>(d, n_systems, experts, weights, index, out, st, s);
-  else
-    launch_mix<1, TE, TO>(d, n_systems, experts, weights, index, out, st, s);
+    return launch_mix<8, TE, TO>(d, n_systems, experts, weights, index, out, st, s);
+  if (vec) return launch_mix<4, TE, TO>(d, n_systems, experts, weights, index, out, st, s);
+  return launch_mix<1, TE, TO>(d, n_systems, experts, weights, index, out, st, s);
 }
 
 template <int COLS, typename TE>
@@ -770,15 +808,12 @@ so2_status so2conv_mix_experts_forward(const so2conv_mix_desc *d, int64_t n_syst
   typedef __nv_bfloat16 bf;
   const bool vec = d->n_weights % 4 == 0 && aligned_to(experts, 4 * es) && aligned_to(out, 4 * os);
   if (d->expert_dtype == SO2_F32 && d->out_dtype == SO2_F32)
-    launch_mix<float, float>(vec, d, n_systems, experts, weights, index, out, st, s);
-  else if (d->expert_dtype == SO2_F32)
-    launch_mix<float, bf>(vec, d, n_systems, experts, weights, index, out, st, s);
-  else if (d->out_dtype == SO2_F32)
-    launch_mix<bf, float>(vec, d, n_systems, experts, weights, index, out, st, s);
-  else
-    launch_mix<bf, bf>(vec, d, n_systems, experts, weights, index, out, st, s);
-  MODEL_CKL();
-  return SO2_OK;
+    return launch_mix<float, float>(vec, d, n_systems, experts, weights, index, out, st, s);
+  if (d->expert_dtype == SO2_F32)
+    return launch_mix<float, bf>(vec, d, n_systems, experts, weights, index, out, st, s);
+  if (d->out_dtype == SO2_F32)
+    return launch_mix<bf, float>(vec, d, n_systems, experts, weights, index, out, st, s);
+  return launch_mix<bf, bf>(vec, d, n_systems, experts, weights, index, out, st, s);
 }
 
 so2_status so2conv_mix_experts_backward(const so2conv_mix_desc *d, int64_t n_systems,
@@ -833,11 +868,11 @@ so2_status so2conv_mix_experts_backward(const so2conv_mix_desc *d, int64_t n_sys
     int64_t rows = ceil_div(MODEL_SMS * 8, cols);
     if (rows > K) rows = K;
     const dim3 grid((unsigned)cols, (unsigned)rows);
-    if (!index && vec)
-      launch_rows<4>(K, (int)n_systems, n, weights, 1, k, grad_out, grad_experts, s);
-    else if (!index)
-      launch_rows<1>(K, (int)n_systems, n, weights, 1, k, grad_out, grad_experts, s);
-    else if (vec)
+    if (!index) {
+      r = vec ? launch_rows<4>(K, (int)n_systems, n, weights, 1, k, grad_out, grad_experts, st, s)
+              : launch_rows<1>(K, (int)n_systems, n, weights, 1, k, grad_out, grad_experts, st, s);
+      if (r != SO2_OK) return r;
+    } else if (vec)
       k_mix_grad_experts<4><<<grid, 256, 0, s>>>((int)slots, K, k, n, weights, offsets, list,
                                                  grad_out, grad_experts);
     else

@@ -362,6 +362,50 @@ def test_mix(T, K, k, n, experts, out):
         assert set(one) == {name} and torch.equal(one[name], g[name])
 
 
+@pytest.mark.parametrize("experts,out", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("T,K,n", [(16, 32, 128), (33, 31, 4), (64, 64, 1500), (130, 40, 516),
+                                   (65, 17, 300), (20, 256, 260), (24, 300, 132), (40, 33, 40004),
+                                   (100, 129, 1028)])
+def test_mix_large_dense(T, K, n, experts, out):
+    # shapes whose products are matrix products; 40,004 columns make a block take several tiles
+    d, e, w, _, G = _mix_case(T, K, None, n, experts, out, seed=T)
+    got = B.mix_experts_forward(d, _dev(e), _dev(w))
+    ref, mag = M.mix_forward(e, w)
+    _close(got, ref, (K + 2) * U * mag, "out")
+    g = B.mix_experts_backward(d, _dev(e), _dev(w), _dev(G))
+    assert B.check(DEV) == 0
+    (ge, me), (gw, mw) = M.mix_backward(e, w, G)
+    _close(g["grad_experts"], ge, (T + 2) * U * me, "grad_experts")
+    _close(g["grad_weights"], gw, (n + 2) * U * mw, "grad_weights")
+    again = B.mix_experts_backward(d, _dev(e), _dev(w), _dev(G))
+    for name in g:
+        assert torch.equal(g[name], again[name]), name
+
+
+@pytest.mark.parametrize("experts", ["f32", "bf16"])
+def test_mix_infinities_and_nan_stay_in_their_columns(experts):
+    d, e, w, _, G = _mix_case(48, 40, None, 400, experts, "f32", seed=7)
+    big = 3.0e38  # its product with a weight below 1 is finite
+    e[3, 130], e[7, 5], e[9, 300] = math.inf, math.nan, big
+    w[:, 9] *= 0.1 / w[:, 9].abs().max()
+    G[1, 399], G[2, 17] = -math.inf, math.nan
+    got = B.mix_experts_forward(d, _dev(e), _dev(w)).cpu().double()
+    ref = w.double() @ e.double()
+    bad = torch.zeros(400, dtype=torch.bool)
+    bad[[130, 5, 300]] = True
+    assert torch.isfinite(got[:, ~bad]).all()
+    _, mag = M.mix_forward(e[:, ~bad], w)
+    assert ((got - ref)[:, ~bad].abs() <= 42 * U * mag).all()
+    assert torch.equal(got[:, 130], torch.where(w[:, 3] > 0, math.inf, -math.inf).double())
+    assert torch.isnan(got[:, 5]).all()
+    assert ((got - ref)[:, 300].abs() <= 42 * U * (w.double().abs() @ e.double().abs())[:, 300]).all()
+    g = B.mix_experts_backward(d, _dev(torch.zeros_like(e)), _dev(w), _dev(G), need=["grad_experts"])
+    ge = g["grad_experts"].cpu()
+    assert torch.isnan(ge[:, 17]).all() and torch.isinf(ge[:, 399]).all()
+    ge[:, [17, 399]] = 0
+    assert torch.isfinite(ge).all()
+
+
 def test_mix_bad_index_is_skipped_with_a_status():
     d, e, w, index, G = _mix_case(6, 5, 3, 40, "f32", "f32")
     index[1, 0], index[4, 2] = 5, -2
