@@ -39,15 +39,22 @@ __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// v as three bf16 whose sum has 24 bits of it; false if v is not finite or
-// rounds to infinity.
-__device__ __forceinline__ bool split3(float v, __nv_bfloat16 &h, __nv_bfloat16 &m, __nv_bfloat16 &l) {
-  h = __float2bfloat16_rn(v);
-  const float r = v - __bfloat162float(h);
-  m = __float2bfloat16_rn(r);
-  l = __float2bfloat16_rn(r - __bfloat162float(m));
-  return (__float_as_uint(__bfloat162float(h)) & 0x7f800000u) != 0x7f800000u;
+// Two f32 as three pairs of bf16 whose sums have 24 bits of them.  `odd` stays
+// 0 as long as every value is finite and its first part too (the remainder is
+// infinite or NaN otherwise, and 0 times that is NaN).  Conversions in pairs:
+// one instruction, where a single one goes through a slower unit.
+__device__ __forceinline__ void split3(float a, float b, uint32_t &h, uint32_t &m, uint32_t &l, float &odd) {
+  h = pack_bf16x2(a, b);
+  const float ra = a - __uint_as_float(h << 16), rb = b - __uint_as_float(h & 0xffff0000u);
+  odd = fmaf(ra, 0.f, fmaf(rb, 0.f, odd));
+  m = pack_bf16x2(ra, rb);
+  l = pack_bf16x2(ra - __uint_as_float(m << 16), rb - __uint_as_float(m & 0xffff0000u));
 }
+
+// Four columns of a row as they lie in memory.
+template <typename TB> struct Quad;
+template <> struct Quad<float> { float4 v; };
+template <> struct Quad<__nv_bfloat16> { uint2 v; };
 
 // Rows of s a K block holds: 32 for small sums, else 64.
 __host__ __device__ constexpr int mixtc_plane(int KB) { return KB * 256; }  // 128 columns x KB rows, bytes
@@ -81,17 +88,18 @@ __global__ void __launch_bounds__(MIXTC_THREADS, 2)
     tmem_relinquish();
   }
   // M's three parts, MN-major: row s holds 64 r, its 16-byte pieces swizzled by s
-  bool bad = false;
-  for (int i = tid; i < blocks * KB * 64; i += MIXTC_THREADS) {
-    const int s = i >> 6, r = i & 63;
-    const float v = s < S && r < rows ? M[(r0 + r) * mr + s * ms] : 0.f;
-    __nv_bfloat16 p[3];
-    bad |= !split3(v, p[0], p[1], p[2]);
+  float bad = 0.f;
+  for (int i = tid; i < blocks * KB * 32; i += MIXTC_THREADS) {
+    const int s = i >> 5, r = (i & 31) * 2;
+    const float v0 = s < S && r < rows ? M[(r0 + r) * mr + s * ms] : 0.f;
+    const float v1 = s < S && r + 1 < rows ? M[(r0 + r + 1) * mr + s * ms] : 0.f;
+    uint32_t p[3];
+    split3(v0, v1, p[0], p[1], p[2], bad);
     const int at = s * 128 + ((((r >> 3) ^ s) & 7) << 4) + (r & 7) * 2;
 #pragma unroll
-    for (int k = 0; k < 3; ++k) *reinterpret_cast<__nv_bfloat16 *>(m_smem + k * m_plane + at) = p[k];
+    for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(m_smem + k * m_plane + at) = p[k];
   }
-  const bool bad_m = __syncthreads_or(bad);
+  const bool bad_m = __syncthreads_or(bad != bad);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -101,20 +109,20 @@ __global__ void __launch_bounds__(MIXTC_THREADS, 2)
   const int64_t mine = blockIdx.x < tiles ? (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
   const int64_t steps = mine * blocks;
   // A warp's rows of a block: s = w + 8 i, four columns a lane
-  float x[PER][4];
-  auto load = [&](int64_t step) {
-    const int64_t c = (blockIdx.x + step / blocks * gridDim.x) * MIXTC_COLS + lane * 4;
-    const int s0 = (int)(step % blocks) * KB + w;
+  Quad<TB> x[PER];
+  int64_t next_tile = blockIdx.x;  // of the next load
+  int next_kb = 0;
+  auto load = [&]() {
+    const int64_t c = next_tile * MIXTC_COLS + lane * 4;
+    const int s0 = next_kb * KB + w;
+    const TB *from = Bm + s0 * n + c;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int s = s0 + 8 * i;
-      if (s < S && c < n) {
-        load_vec<4>(Bm + s * n + c, x[i]);
-      } else {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) x[i][v] = 0.f;
-      }
+      x[i] = Quad<TB>{};
+      if (s0 + 8 * i < S && c < n)
+        x[i].v = *reinterpret_cast<const decltype(x[i].v) *>(from + 8 * i * n);
     }
+    if (++next_kb == blocks) next_kb = 0, next_tile += gridDim.x;
   };
   const int put = (lane >> 4) * (KB * 128) + w * 128 + ((((lane & 15) >> 1) ^ w) << 4) + (lane & 1) * 8;
   // The tile `t` from tensor memory to C (warps w and w + 4 share its 32
@@ -143,36 +151,34 @@ __global__ void __launch_bounds__(MIXTC_THREADS, 2)
   };
 
   bool ok = true, bad_tile = false, bad_last = false;
-  if (steps > 0) load(0);
+  if (steps > 0) load();
+  int kb = 0;
+  int64_t t = 0;  // of the block's tiles
   for (int64_t step = 0; step < steps; ++step) {
-    const int kb = (int)(step % blocks);
-    const int64_t t = step / blocks;
     // the previous step's MMAs have read the operand and written their tile
     if (step > 0) ok = mbar_wait(bar, (uint32_t)(step - 1) & 1, st);
     if (kb == 0) bad_last = bad_tile, bad_tile = bad_m;
-    bool odd = false;
+    float odd = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       uint8_t *to = a_smem + put + i * 1024;
       if constexpr (PARTS == 1) {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) odd |= (__float_as_uint(x[i][v]) & 0x7f800000u) == 0x7f800000u;
-        *reinterpret_cast<uint2 *>(to) =
-            make_uint2(pack_bf16x2(x[i][0], x[i][1]), pack_bf16x2(x[i][2], x[i][3]));
+        const uint2 v = x[i].v;
+        odd = fmaf(__uint_as_float(v.x << 16), 0.f, fmaf(__uint_as_float(v.x & 0xffff0000u), 0.f, odd));
+        odd = fmaf(__uint_as_float(v.y << 16), 0.f, fmaf(__uint_as_float(v.y & 0xffff0000u), 0.f, odd));
+        *reinterpret_cast<uint2 *>(to) = v;
       } else {
-        __nv_bfloat16 p[3][4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) odd |= !split3(x[i][v], p[0][v], p[1][v], p[2][v]);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          __nv_bfloat162 q[2] = {__halves2bfloat162(p[k][0], p[k][1]), __halves2bfloat162(p[k][2], p[k][3])};
-          *reinterpret_cast<uint2 *>(to + k * PLANE) = *reinterpret_cast<uint2 *>(q);
-        }
+        uint2 h, m, l;
+        split3(x[i].v.x, x[i].v.y, h.x, m.x, l.x, odd);
+        split3(x[i].v.z, x[i].v.w, h.y, m.y, l.y, odd);
+        *reinterpret_cast<uint2 *>(to) = h;
+        *reinterpret_cast<uint2 *>(to + PLANE) = m;
+        *reinterpret_cast<uint2 *>(to + 2 * PLANE) = l;
       }
     }
     fence_async_shared();  // the operand's stores, before the MMAs read them
     tc_fence_before();     // the tensor memory reads of the tile before the last
-    if (__syncthreads_or(odd || !ok)) {
+    if (__syncthreads_or(odd != odd || !ok)) {
       if (__syncthreads_or(!ok)) {
         ok = false;
         break;
@@ -200,11 +206,12 @@ __global__ void __launch_bounds__(MIXTC_THREADS, 2)
       umma_commit(bar);
     }
     __syncwarp();
-    if (step + 1 < steps) load(step + 1);
+    if (step + 1 < steps) load();
     if (kb == 0 && t > 0) {
       tc_fence_after();
       finish(t - 1, bad_last);
     }
+    if (++kb == blocks) kb = 0, ++t;
   }
   if (steps > 0 && ok) ok = mbar_wait(bar, (uint32_t)(steps - 1) & 1, st);
   if (__syncthreads_or(!ok)) {
