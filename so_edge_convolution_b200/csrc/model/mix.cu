@@ -29,20 +29,6 @@ __device__ __forceinline__ uint64_t pack2(float a, float b) {
 __device__ __forceinline__ void fma2(uint64_t &d, uint64_t a, uint64_t b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
 }
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void *dst, const void *src) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES)
-                 : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <int TT, int V, typename TB, typename TC>
 __global__ void __launch_bounds__(ROWS_THREADS)
     k_mix_rows(int R, int S, int64_t n, const float *__restrict__ M, int64_t mr, int64_t ms,
@@ -267,18 +253,6 @@ constexpr int DOT_PITCH_G = DOT_COLS + 4;  // f32 elements
 template <typename TE> constexpr int dot_pitch_e() { return DOT_COLS + 16 / (int)sizeof(TE); }
 template <typename TE> constexpr int dot_stage_bytes() {
   return DOT_T * DOT_PITCH_G * 4 + DOT_E * dot_pitch_e<TE>() * (int)sizeof(TE);
-}
-
-template <int BYTES>
-__device__ __forceinline__ void copy_async_or_zero(void *dst, const void *src, bool on) {
-  const int have = on ? BYTES : 0;
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(have)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src),
-                 "n"(BYTES), "r"(have)
-                 : "memory");
 }
 
 // One stage: rows [row0, rows) and columns [c0, n) of a matrix, zero outside.
@@ -660,15 +634,14 @@ so2_status launch_rows_fma(int R, int S, int64_t n, const float *M, int64_t mr, 
   return SO2_OK;
 }
 
-template <int N, int KB, typename TB, typename TC>
+template <int N, typename TB, typename TC>
 so2_status launch_rows_tc(int r0, int R, int S, int64_t n, const float *M, int64_t mr, int64_t ms,
                           const TB *B, TC *C, DevStatus *st, cudaStream_t s) {
-  const int blocks = (S + KB - 1) / KB, smem = mixtc_smem<TB>(KB, blocks);
-  MODEL_CK(cudaFuncSetAttribute(k_mix_tc<N, KB, TB, TC>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  const int blocks = (S + MIXTC_KB - 1) / MIXTC_KB, smem = mixtc_smem<TB>(blocks);
+  MODEL_CK(cudaFuncSetAttribute(k_mix_tc<N, TB, TC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   const int64_t tiles = ceil_div(n, MIXTC_COLS);
-  const int64_t most = MODEL_SMS * (smem <= 110 * 1024 ? 2 : 1);
-  k_mix_tc<N, KB, TB, TC><<<(unsigned)(tiles < most ? tiles : most), MIXTC_THREADS, smem, s>>>(
+  const int64_t most = MODEL_SMS * (smem <= 112 * 1024 ? 2 : 1);
+  k_mix_tc<N, TB, TC><<<(unsigned)(tiles < most ? tiles : most), MIXTC_THREADS, smem, s>>>(
       r0, R, S, blocks, n, M, mr, ms, B, C, st);
   MODEL_CKL();
   return SO2_OK;
@@ -680,13 +653,8 @@ so2_status launch_rows(int R, int S, int64_t n, const float *M, int64_t mr, int6
   if constexpr (V == 4) {
     if (S <= MIXTC_MAX_S && (int64_t)R * S >= MIX_TC_FROM * (R + S)) {
       for (int r0 = 0; r0 < R; r0 += MIXTC_ROWS) {
-        so2_status e;
-        if (R - r0 <= 32)
-          e = S <= 32 ? launch_rows_tc<32, 32>(r0, R, S, n, M, mr, ms, B, C, st, s)
-                      : launch_rows_tc<32, 64>(r0, R, S, n, M, mr, ms, B, C, st, s);
-        else
-          e = S <= 32 ? launch_rows_tc<64, 32>(r0, R, S, n, M, mr, ms, B, C, st, s)
-                      : launch_rows_tc<64, 64>(r0, R, S, n, M, mr, ms, B, C, st, s);
+        const so2_status e = R - r0 <= 32 ? launch_rows_tc<32>(r0, R, S, n, M, mr, ms, B, C, st, s)
+                                          : launch_rows_tc<64>(r0, R, S, n, M, mr, ms, B, C, st, s);
         if (e != SO2_OK) return e;
       }
       return SO2_OK;

@@ -10,9 +10,9 @@
 // first part and needs three.  128 columns of B are the MMA's M, up to 64 rows
 // of C its N, s its K, so both operands are MN-major and B's rows go to shared
 // memory as they lie in memory: a thread splits four columns of a row into
-// three 8-byte stores, with the 128-byte swizzle the MMA reads.  The next
-// step's loads are in flight during the MMAs and during the previous tile's
-// way from tensor memory to C; two blocks an SM overlap the rest.
+// three 8-byte stores, with the 128-byte swizzle the MMA reads.  While a tile's
+// MMAs run, the previous tile goes from tensor memory to C; two blocks an SM
+// overlap the rest.
 //
 // Infinities, NaN and values that round to infinity in bf16 do not survive
 // the split (infinity times a zero part is NaN), so a tile or a matrix M that
@@ -51,36 +51,66 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t &h, uint32_t &
   l = pack_bf16x2(ra - __uint_as_float(m << 16), rb - __uint_as_float(m & 0xffff0000u));
 }
 
-// Four columns of a row as they lie in memory.
-template <typename TB> struct Quad;
-template <> struct Quad<float> { float4 v; };
-template <> struct Quad<__nv_bfloat16> { uint2 v; };
-
-// Rows of s a K block holds: 32 for small sums, else 64.
-__host__ __device__ constexpr int mixtc_plane(int KB) { return KB * 256; }  // 128 columns x KB rows, bytes
+// A step: 32 rows of B by 128 columns.  Its bytes arrive through a ring of
+// asynchronous copies, MIXTC_RING steps deep, of which a thread reads only what
+// it copied itself (four columns of four rows): with the next step's loads in
+// registers instead, 157 MB arrived at 3 TB/s.
+constexpr int MIXTC_KB = 32, MIXTC_RING = 2, MIXTC_PER = MIXTC_KB / 8;
+constexpr int MIXTC_PLANE = MIXTC_KB * 256;  // one part of a step as bf16, bytes
 template <typename TB> constexpr int mixtc_parts() { return sizeof(TB) == 2 ? 1 : 3; }
+template <typename TB> constexpr int mixtc_raw() { return MIXTC_KB * MIXTC_COLS * (int)sizeof(TB); }
 template <typename TB>
-inline int mixtc_smem(int KB, int blocks) {
-  return 1024 + mixtc_parts<TB>() * mixtc_plane(KB) + 3 * blocks * KB * 128 + 64;
+inline int mixtc_smem(int blocks) {
+  return 1024 + 2 * mixtc_parts<TB>() * MIXTC_PLANE + 3 * blocks * MIXTC_KB * 128 +
+         MIXTC_RING * mixtc_raw<TB>() + 64;
 }
 
-// Rows r0 .. r0 + min(R - r0, N) of C; N is 32 or 64, `blocks` the K blocks of S.
-template <int N, int KB, typename TB, typename TC>
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *dst, const void *src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES)
+                 : "memory");
+}
+// The same, or zeros.
+template <int BYTES>
+__device__ __forceinline__ void copy_async_or_zero(void *dst, const void *src, bool on) {
+  const int have = on ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(have)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src),
+                 "n"(BYTES), "r"(have)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows r0 .. r0 + min(R - r0, N) of C; N is 32 or 64, `blocks` the steps of a tile.
+template <int N, typename TB, typename TC>
 __global__ void __launch_bounds__(MIXTC_THREADS, 2)
     k_mix_tc(int r0, int R, int S, int blocks, int64_t n, const float *__restrict__ M, int64_t mr,
              int64_t ms, const TB *__restrict__ Bm, TC *__restrict__ C, DevStatus *st) {
   extern __shared__ uint8_t raw[];
-  constexpr int PARTS = mixtc_parts<TB>(), PLANE = mixtc_plane(KB), PER = KB / 8;
+  constexpr int PARTS = mixtc_parts<TB>(), KB = MIXTC_KB, PLANE = MIXTC_PLANE, PER = MIXTC_PER;
+  constexpr int QUAD = 4 * (int)sizeof(TB);
   uint8_t *a_smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *m_smem = a_smem + PARTS * PLANE;       // [3][blocks][KB rows of 64 r]
+  uint8_t *m_smem = a_smem + 2 * PARTS * PLANE;   // [3][blocks][KB rows of 64 r]
   const int m_plane = blocks * KB * 128;
-  uint64_t *bar = reinterpret_cast<uint64_t *>(m_smem + 3 * m_plane);
-  uint32_t *slot = reinterpret_cast<uint32_t *>(bar + 1);
+  uint8_t *ring = m_smem + 3 * m_plane;           // [MIXTC_RING][PER][threads] four columns
+  uint64_t *bar = reinterpret_cast<uint64_t *>(ring + MIXTC_RING * mixtc_raw<TB>());  // [2]
+  uint32_t *slot = reinterpret_cast<uint32_t *>(bar + 2);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int rows = R - r0 < N ? R - r0 : N;
 
   if (tid == 0) {
     mbar_init(bar, 1);
+    mbar_init(bar + 1, 1);
     fence_mbar_init();
   }
   if (w == 0) {
@@ -109,19 +139,27 @@ __global__ void __launch_bounds__(MIXTC_THREADS, 2)
   const int64_t mine = blockIdx.x < tiles ? (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
   const int64_t steps = mine * blocks;
   // A warp's rows of a block: s = w + 8 i, four columns a lane
-  Quad<TB> x[PER];
-  int64_t next_tile = blockIdx.x;  // of the next load
+  int64_t next_tile = blockIdx.x;  // of the next copy
   int next_kb = 0;
-  auto load = [&]() {
-    const int64_t c = next_tile * MIXTC_COLS + lane * 4;
-    const int s0 = next_kb * KB + w;
-    const TB *from = Bm + s0 * n + c;
+  uint8_t *const own = ring + tid * QUAD;
+  auto copy = [&](int64_t step) {
+    if (next_tile < tiles) {
+      const int64_t c = next_tile * MIXTC_COLS + lane * 4;
+      const int s0 = next_kb * KB + w;
+      const TB *from = Bm + s0 * n + c;
+      uint8_t *to = own + (int)(step % MIXTC_RING) * mixtc_raw<TB>();
+      if (c < n && s0 + 8 * (PER - 1) < S) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      x[i] = Quad<TB>{};
-      if (s0 + 8 * i < S && c < n)
-        x[i].v = *reinterpret_cast<const decltype(x[i].v) *>(from + 8 * i * n);
+        for (int i = 0; i < PER; ++i, from += 8 * n) copy_async<QUAD>(to + i * MIXTC_THREADS * QUAD, from);
+      } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i, from += 8 * n) {
+          const bool on = s0 + 8 * i < S && c < n;
+          copy_async_or_zero<QUAD>(to + i * MIXTC_THREADS * QUAD, on ? from : Bm, on);
+        }
+      }
     }
+    copy_commit();
     if (++next_kb == blocks) next_kb = 0, next_tile += gridDim.x;
   };
   const int put = (lane >> 4) * (KB * 128) + w * 128 + ((((lane & 15) >> 1) ^ w) << 4) + (lane & 1) * 8;
@@ -139,38 +177,50 @@ __global__ void __launch_bounds__(MIXTC_THREADS, 2)
       }
       return;
     }
-    uint32_t v[N / 2];
-    const uint32_t from = tmem + ((uint32_t)(w & 3) << 21) + (uint32_t)(t & 1) * N + ra;
-    if constexpr (N == 64) tmem_ld32(from, v);
-    else tmem_ld16(from, v);
-    if (c >= n) return;
     TC *to = C + (int64_t)(r0 + ra) * n + c;
+    const int left = c < n ? rows - ra : 0;
 #pragma unroll
-    for (int r = 0; r < N / 2; ++r)
-      if (ra + r < rows) to[r * n] = from_f32<TC>(__uint_as_float(v[r]));
+    for (int q = 0; q < N / 2; q += 16) {
+      uint32_t v[16];
+      tmem_ld16(tmem + ((uint32_t)(w & 3) << 21) + (uint32_t)(t & 1) * N + ra + q, v);
+      if (left >= q + 16) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r, to += n) *to = from_f32<TC>(__uint_as_float(v[r]));
+      } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r, to += n)
+          if (q + r < left) *to = from_f32<TC>(__uint_as_float(v[r]));
+      }
+    }
   };
 
+  auto done = [&](int64_t step) { return mbar_wait(bar + (step & 1), (uint32_t)(step >> 1) & 1, st); };
   bool ok = true, bad_tile = false, bad_last = false;
-  if (steps > 0) load();
+#pragma unroll
+  for (int i = 0; i < MIXTC_RING - 1; ++i) copy(i);
   int kb = 0;
   int64_t t = 0;  // of the block's tiles
   for (int64_t step = 0; step < steps; ++step) {
-    // the previous step's MMAs have read the operand and written their tile
-    if (step > 0) ok = mbar_wait(bar, (uint32_t)(step - 1) & 1, st);
+    // the MMAs of the step before the last have read their operand's buffer
+    if (step > 1) ok = ok && done(step - 2);
     if (kb == 0) bad_last = bad_tile, bad_tile = bad_m;
+    copy(step + MIXTC_RING - 1);  // into the slot that the last step has read
+    copy_wait<MIXTC_RING - 1>();
+    const uint8_t *mine_raw = own + (int)(step % MIXTC_RING) * mixtc_raw<TB>();
     float odd = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      uint8_t *to = a_smem + put + i * 1024;
+      uint8_t *to = a_smem + (int)(step & 1) * (PARTS * PLANE) + put + i * 1024;
       if constexpr (PARTS == 1) {
-        const uint2 v = x[i].v;
+        const uint2 v = *reinterpret_cast<const uint2 *>(mine_raw + i * MIXTC_THREADS * QUAD);
         odd = fmaf(__uint_as_float(v.x << 16), 0.f, fmaf(__uint_as_float(v.x & 0xffff0000u), 0.f, odd));
         odd = fmaf(__uint_as_float(v.y << 16), 0.f, fmaf(__uint_as_float(v.y & 0xffff0000u), 0.f, odd));
         *reinterpret_cast<uint2 *>(to) = v;
       } else {
+        const float4 v = *reinterpret_cast<const float4 *>(mine_raw + i * MIXTC_THREADS * QUAD);
         uint2 h, m, l;
-        split3(x[i].v.x, x[i].v.y, h.x, m.x, l.x, odd);
-        split3(x[i].v.z, x[i].v.w, h.y, m.y, l.y, odd);
+        split3(v.x, v.y, h.x, m.x, l.x, odd);
+        split3(v.z, v.w, h.y, m.y, l.y, odd);
         *reinterpret_cast<uint2 *>(to) = h;
         *reinterpret_cast<uint2 *>(to + PLANE) = m;
         *reinterpret_cast<uint2 *>(to + 2 * PLANE) = l;
@@ -189,7 +239,7 @@ __global__ void __launch_bounds__(MIXTC_THREADS, 2)
       tc_fence_after();
       constexpr uint32_t idesc = idesc_bf16_f32(128, N, true);
       const uint32_t d = tmem + (uint32_t)(t & 1) * N;
-      const uint32_t a0 = smem_u32(a_smem), b0 = smem_u32(m_smem) + kb * KB * 128;
+      const uint32_t a0 = smem_u32(a_smem) + (uint32_t)(step & 1) * (PARTS * PLANE), b0 = smem_u32(m_smem) + kb * KB * 128;
       constexpr int ORDER[6][2] = {{0, 2}, {2, 0}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};  // parts of B, of M
       uint32_t more = kb > 0;
 #pragma unroll
@@ -203,17 +253,18 @@ __global__ void __launch_bounds__(MIXTC_THREADS, 2)
           more = 1;
         }
       }
-      umma_commit(bar);
+      umma_commit(bar + (step & 1));
     }
     __syncwarp();
-    if (step + 1 < steps) load();
-    if (kb == 0 && t > 0) {
+    if (kb == 0 && t > 0) {  // (a wait that gave up shows at the next step's barrier)
+      ok = __all_sync(0xffffffffu, done(step - 1));
       tc_fence_after();
-      finish(t - 1, bad_last);
+      if (ok) finish(t - 1, bad_last);
     }
     if (++kb == blocks) kb = 0, ++t;
   }
-  if (steps > 0 && ok) ok = mbar_wait(bar, (uint32_t)(steps - 1) & 1, st);
+  copy_wait<0>();
+  if (steps > 0 && ok) ok = done(steps - 1);
   if (__syncthreads_or(!ok)) {
     // a wait gave up (recorded in the status word): give the MMAs in flight a
     // while longer before their tensor memory is freed
