@@ -248,26 +248,61 @@ __global__ void __launch_bounds__(256)
 // four columns for 64 of them.  Four groups of 64 threads take every fourth
 // vector.  Row pitches are 4 words off a multiple of 32, so the eight rows of
 // a warp's read lie in different banks.
-constexpr int DOT_T = 64, DOT_E = 32, DOT_COLS = 64, DOT_STAGES = 3;
+constexpr int DOT_T = 64, DOT_E = 32, DOT_COLS = 64, DOT_STAGES = 4;
 constexpr int DOT_PITCH_G = DOT_COLS + 4;  // f32 elements
 template <typename TE> constexpr int dot_pitch_e() { return DOT_COLS + 16 / (int)sizeof(TE); }
 template <typename TE> constexpr int dot_stage_bytes() {
   return DOT_T * DOT_PITCH_G * 4 + DOT_E * dot_pitch_e<TE>() * (int)sizeof(TE);
 }
 
-// One stage: rows [row0, rows) and columns [c0, n) of a matrix, zero outside.
+// A thread's vectors of a stage: one column group of ROWS / 16 rows, 16 apart.
+// Rows and columns outside the matrix are zero.  (VEC: vectors of four and
+// asynchronous copies; otherwise single values, 64 of them side by side.)
 template <int ROWS, int PITCH, bool VEC, typename T>
-__device__ __forceinline__ void dot_load(T *dst, const T *src, int row0, int rows, int64_t c0, int64_t n) {
-  constexpr int V = VEC ? 4 : 1, PER_ROW = DOT_COLS / V;
-  for (int i = threadIdx.x; i < ROWS * PER_ROW; i += 256) {
-    const int r = i / PER_ROW, c = (i % PER_ROW) * V;
-    const bool on = row0 + r < rows && c0 + c < n;
-    const T *from = on ? src + (int64_t)(row0 + r) * n + c0 + c : src;
-    if constexpr (VEC)
-      copy_async_or_zero<V * (int)sizeof(T)>(dst + r * PITCH + c, from, on);
-    else
-      dst[r * PITCH + c] = on ? *from : from_f32<T>(0.f);
+struct DotLoader {
+  static constexpr int V = VEC ? 4 : 1, PER_ROW = DOT_COLS / V, APART = 256 / PER_ROW,
+                       COUNT = ROWS / APART;
+  const T *from;  // the thread's first vector of the next stage
+  int64_t c, n;   // its column
+  int rows;       // of its rows inside the matrix
+  int put;
+  __device__ __forceinline__ DotLoader(const T *src, int row0, int limit, int64_t c0, int64_t n_) : n(n_) {
+    const int r = threadIdx.x / PER_ROW;
+    c = c0 + threadIdx.x % PER_ROW * V;
+    from = src + (int64_t)(row0 + r) * n + c;
+    rows = (limit - row0 - r + APART - 1) / APART;  // may be 0 or less
+    put = r * PITCH + threadIdx.x % PER_ROW * V;
   }
+  __device__ __forceinline__ void load(T *dst, const T *base) {
+    const T *p = from;
+    if (VEC && rows >= COUNT && c < n) {
+#pragma unroll
+      for (int k = 0; k < COUNT; ++k, p += APART * n)
+        copy_async<V * (int)sizeof(T)>(dst + put + k * APART * PITCH, p);
+    } else {
+#pragma unroll
+      for (int k = 0; k < COUNT; ++k, p += APART * n) {
+        const bool on = k < rows && c < n;
+        if constexpr (VEC)
+          copy_async_or_zero<V * (int)sizeof(T)>(dst + put + k * APART * PITCH, on ? p : base, on);
+        else
+          dst[put + k * APART * PITCH] = on ? *p : from_f32<T>(0.f);
+      }
+    }
+    from += DOT_COLS;
+    c += DOT_COLS;
+  }
+};
+
+// Four columns of an operand row as two packed pairs.
+__device__ __forceinline__ void dot_read(const float *p, uint64_t (&v)[2]) {
+  const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(p);
+  v[0] = q.x, v[1] = q.y;
+}
+__device__ __forceinline__ void dot_read(const __nv_bfloat16 *p, uint64_t (&v)[2]) {
+  float f[4];
+  load_vec<4>(p, f);
+  v[0] = pack2(f[0], f[1]), v[1] = pack2(f[2], f[3]);
 }
 
 // part[split][t][e], with blockIdx.x the split, blockIdx.y the tile.
@@ -283,14 +318,16 @@ __global__ void __launch_bounds__(256, 2)
   const int t0 = (blockIdx.y / etiles) * DOT_T, e0 = (blockIdx.y % etiles) * DOT_E;
   const int64_t tiles = (n + DOT_COLS - 1) / DOT_COLS;
   const int64_t first = tiles * blockIdx.x / gridDim.x, last = tiles * (blockIdx.x + 1) / gridDim.x;
-  auto g_of = [&](int64_t i) { return reinterpret_cast<float *>(sm + (i % DOT_STAGES) * STAGE); };
+  auto g_of = [&](int64_t i) { return reinterpret_cast<float *>(sm + (int)((i - first) % DOT_STAGES) * STAGE); };
   auto e_of = [&](int64_t i) {
-    return reinterpret_cast<TE *>(sm + (i % DOT_STAGES) * STAGE + DOT_T * DOT_PITCH_G * 4);
+    return reinterpret_cast<TE *>(sm + (int)((i - first) % DOT_STAGES) * STAGE + DOT_T * DOT_PITCH_G * 4);
   };
+  DotLoader<DOT_T, DOT_PITCH_G, VEC, float> lg(grad, t0, T, first * DOT_COLS, n);
+  DotLoader<DOT_E, PE, VEC, TE> le(experts, e0, K, first * DOT_COLS, n);
   auto load = [&](int64_t i) {
     if (i < last) {
-      dot_load<DOT_T, DOT_PITCH_G, VEC>(g_of(i), grad, t0, T, i * DOT_COLS, n);
-      dot_load<DOT_E, PE, VEC>(e_of(i), experts, e0, K, i * DOT_COLS, n);
+      lg.load(g_of(i), grad);
+      le.load(e_of(i), experts);
     }
     copy_commit();
   };
@@ -311,16 +348,9 @@ __global__ void __launch_bounds__(256, 2)
     for (int q = cg; q < DOT_COLS / 4; q += 4) {
       uint64_t gv[8][2], xv[4][2];
 #pragma unroll
-      for (int a = 0; a < 8; ++a) {
-        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(g + (tg + 8 * a) * DOT_PITCH_G + 4 * q);
-        gv[a][0] = v.x, gv[a][1] = v.y;
-      }
+      for (int a = 0; a < 8; ++a) dot_read(g + (tg + 8 * a) * DOT_PITCH_G + 4 * q, gv[a]);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        float f[4];
-        load_vec<4>(x + (eg + 8 * b) * PE + 4 * q, f);
-        xv[b][0] = pack2(f[0], f[1]), xv[b][1] = pack2(f[2], f[3]);
-      }
+      for (int b = 0; b < 4; ++b) dot_read(x + (eg + 8 * b) * PE + 4 * q, xv[b]);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
