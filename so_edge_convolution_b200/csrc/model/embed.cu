@@ -449,9 +449,11 @@ bool embed_ok(const so2conv_embed_desc *d) {
 
 // Tokens few enough that every table row looks at all of them: the scans are
 // n_rows * n / 32 steps of a warp, and a row's own tokens one eighth of n deep
-// at worst.  It is one launch where the sort takes six.
+// at worst.  Scan / sort in us at 128 channels: 100 rows, 128 tokens 2.3 / 12.3,
+// 2,048 11.5 / 17.9, 4,096 18.1 / 19.3, 8,192 37.4 / 18.4; 2,000 rows, 2,048
+// tokens 9.3 / 26.
 bool embed_scans(const so2conv_embed_desc *d, int64_t n) {
-  return n <= 2048 && d->n_rows * n <= (1 << 20);
+  return n <= 4096 && d->n_rows * n <= (1 << 22);
 }
 
 // Lanes that take a row of `vectors` vectors, as a power of two.

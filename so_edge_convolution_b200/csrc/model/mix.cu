@@ -17,9 +17,11 @@ namespace so2 {
 constexpr int ROWS_THREADS = 128;
 constexpr int ROWS_SC = 32;     // rows of B whose weights are staged together
 constexpr int ROWS_DEPTH = 8;   // copies in flight
-// From R S / (R + S) on (the FMAs over the bytes) the tensor cores take the
-// product (mix_tc.cuh).
-constexpr int MIX_TC_FROM = 10;
+// From this many FMAs a column (R S) on the tensor cores take the product
+// (mix_tc.cuh), whose tiles cost much the same whatever they hold.  Forward of
+// 1,228,800 f32 columns, FMA / tensor us: 24 x 24 50 / 66, 32 x 16 53 / 64,
+// 32 x 32 82 / 64, 64 x 16 97 / 79, 64 x 64 283 / 125.
+constexpr int MIX_TC_FROM = 768;
 
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(256)
 
 // ---- the routing weights' gradient: products over all columns --------------------------
 // Every (t, e) of a tile of 64 systems and 32 experts, over the block's share
-// of the columns.  Tiles of both operands go through shared memory in three
+// of the columns.  Tiles of both operands go through shared memory in four
 // stages of asynchronous copies; a thread holds 8 x 4 products, two columns to
 // a packed FMA (their halves are added at the end), and reads 12 vectors of
 // four columns for 64 of them.  Four groups of 64 threads take every fourth
@@ -592,17 +594,18 @@ MixPlan mix_plan(const so2conv_mix_desc *d, int64_t n_systems, int which) {
     const size_t slots = (size_t)(n_systems * d->top_k);
     p.offsets = ws_take(c, sizeof(int) * (d->n_experts + 1));
     p.list = ws_take(c, sizeof(int) * slots);
-    // A product costs a tile about an eighth of what it costs by slot (12
-    // vector reads for 256 products against 2 for 4), so tiles where the slots
-    // name that share of the experts.
-    p.tiles = d->top_k * 8 >= d->n_experts;
+    // The products of all (t, e) in tiles, or of the slots one by one.  Both
+    // gradients of 307,200 bf16 weights, tiles / slots in us: 33 systems, 4 of
+    // 64 experts 121 / 66, 8 of 64 128 / 95, 16 of 64 155 / 137.
+    p.tiles = d->top_k * 2 >= d->n_experts;
     const int64_t per = p.tiles ? n_systems * d->n_experts : n_systems * d->top_k;  // products
     int64_t want;
-    // All systems' gradients of at least 128 columns in a block's shared memory
-    // (two blocks an SM): 33 systems, top 4 of 64, 307,200 weights take 30 us
-    // for both gradients where the separate kernels take 58.
+    // Up to eight slots a system, and all systems' gradients of at least 128
+    // columns in a block's shared memory (two blocks an SM): one kernel for both
+    // gradients.  Same case, together / apart in us: 2 of 64 51 / 59, 4 of 64
+    // 63 / 66, 8 of 64 86 / 95, but 16 of 64 174 / 137.
     p.cols = 0;
-    if (!p.tiles && n_systems > 0 && slots <= BACK_SLOTS && d->n_experts <= BACK_EXPERTS &&
+    if (!p.tiles && n_systems > 0 && d->top_k <= 8 && slots <= BACK_SLOTS && d->n_experts <= BACK_EXPERTS &&
         d->n_weights % 4 == 0) {
       p.cols = 512;
       while (p.cols >= 128 && n_systems * p.cols * 8 > BACK_BYTES) p.cols /= 2;
@@ -681,7 +684,7 @@ template <int V, typename TB, typename TC>
 so2_status launch_rows(int R, int S, int64_t n, const float *M, int64_t mr, int64_t ms, const TB *B,
                        TC *C, DevStatus *st, cudaStream_t s) {
   if constexpr (V == 4) {
-    if (S <= MIXTC_MAX_S && (int64_t)R * S >= MIX_TC_FROM * (R + S)) {
+    if (S <= MIXTC_MAX_S && (int64_t)R * S >= MIX_TC_FROM) {
       for (int r0 = 0; r0 < R; r0 += MIXTC_ROWS) {
         const so2_status e = R - r0 <= 32 ? launch_rows_tc<32>(r0, R, S, n, M, mr, ms, B, C, st, s)
                                           : launch_rows_tc<64>(r0, R, S, n, M, mr, ms, B, C, st, s);

@@ -309,6 +309,7 @@ def test_route_many_rows_and_none():
 
 # ---- mixing ------------------------------------------------------------------------
 MIX = [  # systems, experts, slots (None: every expert in order), weights
+    (6, 40, 12, 260), (9, 30, 16, 132), (97, 50, 3, 132), (40, 20, 2, 1028),
     (1, 1, None, 1), (1, 32, None, 4864), (3, 5, None, 33), (2, 7, 3, 130), (33, 64, 4, 1000),
     (64, 32, None, 2052), (17, 9, 9, 515), (5, 130, None, 257), (70, 3, 2, 96), (130, 40, 5, 260),
     (4, 8, 2, 70001), (9, 128, None, 1028),
@@ -568,6 +569,38 @@ def test_the_operators_around_the_convolution():
         # the convolution's own tolerance on its f32 path, over the chain's few steps
         err = (got.double().cpu() - ref).abs().max() / ref.abs().max()
         assert err < 4e-4, (name, float(err))
+
+
+def test_offsets_beyond_32_bits():
+    # one tensor of over 2^31 elements at a time; the far end is looked at
+    n, c = 34000, 65536
+    d = B.make_dropout_desc(c, 1, "element", 0.5, B.SO2_BF16)
+    x = torch.ones((n, 1, c), dtype=torch.bfloat16, device=DEV)
+    rng = torch.tensor([3, 4], device=DEV)
+    B.dropout(d, x, rng, out=x)
+    keep = [M.philox((m // 4) | (4 << 64), 3)[m % 4] >= 1 << 31
+            for m in range((n - 1) * c, (n - 1) * c + 64)]
+    assert x[n - 1, 0, :64].float().cpu().tolist() == [2.0 if k else 0.0 for k in keep]
+    # embedding rows and their gradient 2^26 elements apart
+    wide = x.view(-1)[: 33 << 26].view(33, 1 << 26)
+    ids = (torch.arange(33) % 5).to(DEV)
+    t = torch.randn((5, 48), generator=_gen(1)).to(DEV)
+    ed = B.make_embed_desc(5, 48, out_dtype=B.SO2_BF16)
+    B.embed_forward(ed, ids, t, out=wide[:, 64:112].unflatten(1, (1, 48)))
+    assert torch.equal(wide[:, 64:112].cpu(), t.bfloat16()[ids].cpu())
+    gt = B.embed_backward(ed, ids, wide[:, 64:112])
+    _check_embed_grad(gt, ids.cpu(), wide[:, None, 64:112].cpu(), 5, None, 1.0)
+    # 33 experts of 2^26 weights, by index and in order
+    w = torch.randn((1, 33), generator=_gen(2)).to(DEV)
+    e = wide[:, -8:].float().cpu()
+    for k, index in ((33, None), (2, torch.tensor([[32, 31]], dtype=torch.int32, device=DEV))):
+        md = B.make_mix_desc(33, 1 << 26, k, B.SO2_BF16, B.SO2_F32)
+        got = B.mix_experts_forward(md, wide, w[:, :k].contiguous(), index=index)
+        ref, mag = M.mix_forward(e, w[:, :k].cpu(), index)
+        _close(got[:, -8:], ref, (k + 2) * U * mag, "out")
+    G = torch.ones((1, 1 << 26), device=DEV)
+    g = B.mix_experts_backward(md, wide, w[:, :2].contiguous(), G, index=index)
+    assert (g["grad_experts"][32] == w[0, 0]).all() and (g["grad_experts"][:31] == 0).all()
 
 
 def _all_ops(s):
