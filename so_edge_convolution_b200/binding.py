@@ -538,6 +538,11 @@ def _need(t, name, shape, dtype, device=None):
     return t if t.is_contiguous() else t.contiguous()
 
 
+def _adr(t):
+    """A checked tensor's address, for a pointer argument."""
+    return None if t is None else t.data_ptr()
+
+
 def _on_device(t, name, device):
     if not t.is_cuda or (device is not None and t.device != device):
         raise ValueError(f"{name} must be on {device or 'a CUDA device'}, not {t.device}")
@@ -587,8 +592,8 @@ def embed_forward(desc, ids, table, out=None, ws=None):
     ld = _rows_of(out, n, desc.n_comp * desc.channels, "out")
     need = lib.so2conv_embed_workspace_size(ctypes.byref(desc), n, WS_FORWARD)
     p, nb = _model_ws(need, "embed_workspace_size", dev, ws)
-    _run(dev, "so2conv_embed_forward", lib.so2conv_embed_forward, ctypes.byref(desc), n, _ptr(ids),
-         _ptr(table), out.data_ptr(), ld, p, nb)
+    _run(dev, "so2conv_embed_forward", lib.so2conv_embed_forward, ctypes.byref(desc), n, _adr(ids),
+         _adr(table), out.data_ptr(), ld, p, nb)
     return out
 
 
@@ -615,7 +620,7 @@ def embed_backward(desc, ids, grad_out, out=None, ws=None):
     need = lib.so2conv_embed_workspace_size(ctypes.byref(desc), n, WS_BACKWARD)
     p, nb = _model_ws(need, "embed_workspace_size", dev, ws)
     _run(dev, "so2conv_embed_backward", lib.so2conv_embed_backward, ctypes.byref(desc), n,
-         _ptr(ids), grad_out.data_ptr(), ld, _ptr(out), p, nb)
+         _adr(ids), grad_out.data_ptr(), ld, _adr(out), p, nb)
     return out
 
 
@@ -638,7 +643,7 @@ def route_forward(desc, logits, bias=None):
     index = torch.empty_like(weights, dtype=torch.int32)
     counts = index.new_empty(desc.n_experts)
     _run(dev, "so2conv_route_forward", lib.so2conv_route_forward, ctypes.byref(desc), n,
-         _ptr(logits), _ptr(bias), _ptr(weights), _ptr(index), _ptr(counts))
+         _adr(logits), _adr(bias), _adr(weights), _adr(index), _adr(counts))
     return weights, index, counts
 
 
@@ -652,7 +657,7 @@ def route_backward(desc, logits, index, grad_weights, out=None):
     grad_weights = _need(grad_weights, "grad_weights", (n, desc.top_k), torch.float32, dev)
     out = _given_out(out, "out", (n, desc.n_experts), torch.float32, logits)
     _run(dev, "so2conv_route_backward", lib.so2conv_route_backward, ctypes.byref(desc), n,
-         _ptr(logits), _ptr(index), _ptr(grad_weights), _ptr(out))
+         _adr(logits), _adr(index), _adr(grad_weights), _adr(out))
     return out
 
 
@@ -680,7 +685,7 @@ def mix_experts_forward(desc, experts, weights, index=None, out=None, ws=None):
     need = lib.so2conv_mix_workspace_size(ctypes.byref(desc), n, WS_FORWARD)
     p, nb = _model_ws(need, "mix_workspace_size", dev, ws)
     _run(dev, "so2conv_mix_experts_forward", lib.so2conv_mix_experts_forward, ctypes.byref(desc), n,
-         _ptr(experts), _ptr(weights), _ptr(index), _ptr(out), p, nb)
+         _adr(experts), _adr(weights), _adr(index), _adr(out), p, nb)
     return out
 
 
@@ -698,8 +703,8 @@ def mix_experts_backward(desc, experts, weights, grad_out, index=None, need=None
     size = lib.so2conv_mix_workspace_size(ctypes.byref(desc), n, WS_BACKWARD)
     p, nb = _model_ws(size, "mix_workspace_size", dev, ws)
     _run(dev, "so2conv_mix_experts_backward", lib.so2conv_mix_experts_backward, ctypes.byref(desc),
-         n, _ptr(experts), _ptr(weights), _ptr(index), _ptr(grad_out),
-         *[_ptr(outs[k]) for k in names], p, nb)
+         n, _adr(experts), _adr(weights), _adr(index), _adr(grad_out),
+         *[_adr(outs[k]) for k in names], p, nb)
     return {k: t for k, t in outs.items() if t is not None}
 
 
@@ -722,6 +727,6 @@ def dropout(desc, x, rng, residual=None, rows=None, out=None):
     if rows is not None:
         rows = _need(rows, "rows", (n,), torch.int64, dev)
     out = _given_out(out, "out", shape, dt, x)
-    _run(dev, "so2conv_dropout", lib.so2conv_dropout, ctypes.byref(desc), n, _ptr(x),
-         _ptr(residual), _ptr(rows), _ptr(rng), _ptr(out))
+    _run(dev, "so2conv_dropout", lib.so2conv_dropout, ctypes.byref(desc), n, _adr(x),
+         _adr(residual), _adr(rows), _adr(rng), _adr(out))
     return out

@@ -34,13 +34,14 @@ __device__ __forceinline__ void fma2(uint64_t &d, uint64_t a, uint64_t b) {
 template <int TT, int V, typename TB, typename TC>
 __global__ void __launch_bounds__(ROWS_THREADS)
     k_mix_rows(int R, int S, int64_t n, const float *__restrict__ M, int64_t mr, int64_t ms,
-               const TB *__restrict__ Bm, TC *__restrict__ C) {
+               const TB *__restrict__ Bm, TC *__restrict__ C, DevStatus *st) {
   constexpr int PAIRS = (TT + 1) / 2;
   constexpr bool RING = V > 1;
   constexpr int BYTES = V * (int)sizeof(TB);
   __shared__ __align__(16) float wts[ROWS_SC][2 * PAIRS];
   __shared__ __align__(16) unsigned char ring[RING ? ROWS_DEPTH : 1][ROWS_THREADS][RING ? BYTES : 4];
   const int tid = threadIdx.x;
+  if (blockIdx.x == 0 && tid == 0) *st = DevStatus{0, 0};  // nothing here can go wrong
   const int64_t c = (blockIdx.x * (int64_t)ROWS_THREADS + tid) * V;
   const bool on = c < n;
   const TB *col = Bm + c;
@@ -173,6 +174,8 @@ __global__ void k_mix_lists(int n_slots, int K, const int *__restrict__ index,
   const int lane = threadIdx.x & 31;
   const int e = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (e >= K) return;
+  if (e == 0 && lane == 0) *st = DevStatus{0, 0};  // this warp alone touches it
+  __syncwarp();
   int lower = 0, mine = 0;
   for (int p0 = 0; p0 < n_slots; p0 += 32) {
     const int p = p0 + lane, v = p < n_slots ? index[p] : -1;
@@ -650,11 +653,11 @@ so2_status mix_checks(const so2conv_mix_desc *d, int64_t n_systems, const void *
 // with evenly filled ones.
 template <int V, typename TB, typename TC>
 so2_status launch_rows_fma(int R, int S, int64_t n, const float *M, int64_t mr, int64_t ms,
-                           const TB *B, TC *C, cudaStream_t s) {
+                           const TB *B, TC *C, DevStatus *st, cudaStream_t s) {
   const unsigned grid = (unsigned)ceil_div(n, ROWS_THREADS * V);
   const int passes = (R + 31) / 32, tt = (R + passes - 1) / passes;
 #define MIX_ROWS(TT) \
-  k_mix_rows<TT, V, TB, TC><<<grid, ROWS_THREADS, 0, s>>>(R, S, n, M, mr, ms, B, C)
+  k_mix_rows<TT, V, TB, TC><<<grid, ROWS_THREADS, 0, s>>>(R, S, n, M, mr, ms, B, C, st)
   if (tt <= 1) MIX_ROWS(1);
   else if (tt <= 2) MIX_ROWS(2);
   else if (tt <= 4) MIX_ROWS(4);
@@ -685,6 +688,7 @@ so2_status launch_rows(int R, int S, int64_t n, const float *M, int64_t mr, int6
                        TC *C, DevStatus *st, cudaStream_t s) {
   if constexpr (V == 4) {
     if (S <= MIXTC_MAX_S && (int64_t)R * S >= MIX_TC_FROM) {
+      MODEL_CK(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
       for (int r0 = 0; r0 < R; r0 += MIXTC_ROWS) {
         const so2_status e = R - r0 <= 32 ? launch_rows_tc<32>(r0, R, S, n, M, mr, ms, B, C, st, s)
                                           : launch_rows_tc<64>(r0, R, S, n, M, mr, ms, B, C, st, s);
@@ -693,7 +697,7 @@ so2_status launch_rows(int R, int S, int64_t n, const float *M, int64_t mr, int6
       return SO2_OK;
     }
   }
-  return launch_rows_fma<V>(R, S, n, M, mr, ms, B, C, s);
+  return launch_rows_fma<V>(R, S, n, M, mr, ms, B, C, st, s);
 }
 
 template <int V, typename TE, typename TO>
@@ -705,6 +709,7 @@ so2_status launch_mix(const so2conv_mix_desc *d, int64_t n_systems, const void *
       return launch_rows<V>((int)n_systems, d->n_experts, d->n_weights, weights, d->top_k, 1,
                             static_cast<const TE *>(experts), static_cast<TO *>(out), st, s);
   }
+  MODEL_CK(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
   const int64_t cols = ceil_div(d->n_weights, 256 * V);
   int64_t rows = ceil_div(MODEL_SMS * 16, cols);
   if (rows > n_systems) rows = n_systems;
@@ -804,8 +809,10 @@ so2_status so2conv_mix_experts_forward(const so2conv_mix_desc *d, int64_t n_syst
   if (n_systems > 0 && (!out || !aligned_to(out, os))) return SO2_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DevStatus *st = ws_at<DevStatus>(ws, p.status);
-  MODEL_CK(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
-  if (n_systems == 0) return SO2_OK;
+  if (n_systems == 0) {
+    MODEL_CK(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
+    return SO2_OK;
+  }
   typedef __nv_bfloat16 bf;
   const bool vec = d->n_weights % 4 == 0 && aligned_to(experts, 4 * es) && aligned_to(out, 4 * os);
   if (d->expert_dtype == SO2_F32 && d->out_dtype == SO2_F32)
@@ -830,7 +837,7 @@ so2_status so2conv_mix_experts_backward(const so2conv_mix_desc *d, int64_t n_sys
     return SO2_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DevStatus *st = ws_at<DevStatus>(ws, p.status);
-  MODEL_CK(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
+  if (!index || n_systems == 0) MODEL_CK(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
   if (n_systems == 0) {
     if (grad_experts)
       MODEL_CK(cudaMemsetAsync(grad_experts, 0, sizeof(float) * d->n_experts * d->n_weights, s));
