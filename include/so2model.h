@@ -95,8 +95,10 @@ so2_status so2conv_embed_backward(const so2conv_embed_desc *desc, int64_t n, con
  * A logit of -inf, or a c of -inf, takes the expert out; slots that are left
  * over hold index -1 and weight 0, and a row without any expert holds nothing
  * else.  A logit of the type's lowest value is an ordinary, very small one.
- * NaN ranks below every number; weights follow the formula.  Chosen sigmoid
- * scores that are all 0 in f32 renormalise to 0.
+ * NaN ranks below every number; weights follow the formula, where softmax with
+ * renormalise is the softmax of the chosen logits (so it does not see logits
+ * that were not chosen, and chosen scores that vanish in f32 keep their
+ * ratios).  Chosen sigmoid scores that are all 0 in f32 renormalise to 0.
  *
  * Backward of <grad_weights, weights> for the choice made: grad_logits f32
  * [n_tokens, n_experts].  An index outside [0, n_experts) is an unused slot:
@@ -138,6 +140,10 @@ so2_status so2conv_route_backward(const so2conv_route_desc *desc, int64_t n_toke
  * An index of -1 is an unused slot: its weight is not used.  The same expert
  * may be named twice.  Another index outside [0, n_experts) is skipped and
  * recorded as SO2_ERR_INDEX.
+ *
+ * Sums are f32 (fused multiply-adds, or tensor-core products of three bf16
+ * parts of each operand, which keep 2^-24 of magnitudes down to 2^-109); NaN
+ * and infinities in an expert or in grad_out reach what the formula says.
  *
  * Backward: with grad_out f32 [n_systems, n_weights] (a convolution's grad_w
  * per system),

@@ -158,3 +158,29 @@ def test_binding_checks_its_tensors():
         B.dropout(B.make_dropout_desc(16, 4), z(3, 4, 15), z(2, dtype=torch.int64))
     with pytest.raises(ValueError):
         B.mix_experts_forward(B.make_mix_desc(4, 10, 2), z(4, 9), z(3, 2))
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    import torch
+    entered = []
+
+    class Guard:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            entered.append(self.device)
+
+        def __exit__(self, *exc):
+            entered.append(None)
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(B, "_stream", lambda device: ("stream", device.index))
+    calls = []
+    for index in (0, 1):
+        B._run(torch.device("cuda", index), "x", lambda *a: calls.append((a, list(entered))) or 0, 7)
+    assert calls[0] == ((7, ("stream", 0)), [])
+    assert calls[1] == ((7, ("stream", 1)), [torch.device("cuda", 1)]) and entered[-1] is None
+    with pytest.raises(B.So2Error):
+        B._run(torch.device("cuda", 0), "x", lambda *a: 5)
