@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(256)
 // copies, forms the experts' gradient there from groups of cols / 4 threads
 // (four columns a thread, an expert a group) and the slots' products from its
 // warps.  grad_out is read once and nothing else passes through L2 twice but
-// the experts' rows that several systems name.  part[tile][slot].
+// the experts' rows that several systems name.  part[block][slot].
 constexpr int BACK_SLOTS = 2048, BACK_EXPERTS = 1024, BACK_BYTES = 96 * 1024;
 
 template <int COLS, typename TE>
@@ -454,6 +454,7 @@ __global__ void __launch_bounds__(256)
   int2 *by_expert = reinterpret_cast<int2 *>(stage + 2 * T * COLS);  // the lists: system's place, weight
   int2 *by_slot = by_expert + slots;                                 // the slots: place, expert or -1
   int *off = reinterpret_cast<int *>(by_slot + slots);               // [K + 1]
+  float *total = reinterpret_cast<float *>(off + K + 1);             // the slots' products so far
   const int64_t tiles = (n + COLS - 1) / COLS;
   auto load = [&](int64_t tile) {
     if (tile < tiles) {
@@ -477,6 +478,7 @@ __global__ void __launch_bounds__(256)
     by_slot[i] = make_int2(i / top_k * COLS, e >= 0 && e < K ? e : -1);
   }
   for (int i = tid; i <= K; i += 256) off[i] = offsets[i];
+  for (int i = tid; i < slots; i += 256) total[i] = 0.f;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     load(tile + gridDim.x);  // into the buffer that the last step is done with
     copy_wait<1>();
@@ -530,13 +532,15 @@ __global__ void __launch_bounds__(256)
         for (int u = 0; u < S; ++u) {
 #pragma unroll
           for (int o = 16; o; o >>= 1) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
-          if (lane == 0 && p + 8 * u < slots) part[tile * slots + p + 8 * u] = sum[u];
+          if (lane == 0 && p + 8 * u < slots) total[p + 8 * u] += sum[u];  // this warp's alone
         }
       }
     }
     __syncthreads();  // everyone is done with this buffer
   }
   copy_wait<0>();
+  if (part)
+    for (int i = tid; i < slots; i += 256) part[blockIdx.x * (int64_t)slots + i] = total[i];
 }
 
 // gw[slot] from the splits: of all (t, e) (all) or of the slots.  A lane a
@@ -575,7 +579,8 @@ namespace {
 struct MixPlan {
   size_t status, offsets, list, part, total;
   bool tiles;  // the products of all (t, e), or of the slots alone
-  int cols;    // both gradients by index together: a block's columns, or 0
+  int cols;    // both gradients by index together: a tile's columns, or 0
+  int smem;    // and the block's shared memory
   int splits;
 };
 
@@ -624,8 +629,14 @@ MixPlan mix_plan(const so2conv_mix_desc *d, int64_t n_systems, int which) {
     // at most 16 M partial sums
     const int64_t most = per > 0 ? (16ll << 20) / per : 1;
     p.splits = (int)(want < most ? want : (most > 0 ? most : 1));
-    // (a block a column range; the partial sums are a part in `cols` of the operands)
-    if (p.cols) p.splits = (int)ceil_div(d->n_weights, p.cols);
+    if (p.cols) {
+      // as many blocks as stay resident, which take equal shares of the tiles
+      p.smem = (int)(n_systems * p.cols * 8 + slots * 20 + (d->n_experts + 1) * 4);
+      int fit = 224 * 1024 / (p.smem + 1024);
+      if (fit > 4) fit = 4;
+      const int64_t tiles = ceil_div(d->n_weights, p.cols);
+      p.splits = (int)ceil_div(tiles, ceil_div(tiles, MODEL_SMS * fit));
+    }
     p.part = ws_take(c, sizeof(float) * (size_t)(per * p.splits));
   }
   p.total = (c + 255) & ~static_cast<size_t>(255);
@@ -737,17 +748,11 @@ so2_status mix_back_slots(const so2conv_mix_desc *d, int64_t T, const MixPlan &p
                           const float *weights, const int32_t *index, const int *offsets,
                           const int *list, const float *grad, float *ge, float *part,
                           cudaStream_t s) {
-  const size_t smem = (size_t)T * COLS * 8 + T * d->top_k * 16 + (d->n_experts + 1) * 4;
   MODEL_CK(cudaFuncSetAttribute(k_mix_back_slots<COLS, TE>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  // as many blocks as stay resident, which then take equal shares of the tiles
-  int fit = (int)(224 * 1024 / (smem + 1024));
-  if (fit > 4) fit = 4;
-  const int64_t steps = ceil_div(p.splits, MODEL_SMS * fit);
-  const unsigned grid = (unsigned)ceil_div(p.splits, steps);
-  k_mix_back_slots<COLS, TE><<<grid, 256, smem, s>>>((int)T, d->n_experts, d->top_k, d->n_weights,
-                                                         experts, weights, index, offsets, list, grad,
-                                                         ge, part);
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem));
+  k_mix_back_slots<COLS, TE><<<p.splits, 256, p.smem, s>>>(
+      (int)T, d->n_experts, d->top_k, d->n_weights, experts, weights, index, offsets, list, grad, ge,
+      part);
   MODEL_CKL();
   return SO2_OK;
 }
