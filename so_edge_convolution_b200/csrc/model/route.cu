@@ -450,6 +450,12 @@ __device__ __forceinline__ void exchange(uint32_t &a, uint32_t &b) {
   b = a > b ? b : a;
   a = hi;
 }
+// The order of numbers (NaN is looked for apart); -inf is the last below WORD_LIVE.
+__device__ __forceinline__ uint32_t plain_key32(float c) {
+  const int b = __float_as_int(c + 0.f);
+  return (uint32_t)b ^ ((uint32_t)(b >> 31) | 0x80000000u);
+}
+constexpr uint32_t WORD_LIVE = 0x00800000u;  // the word of an expert that may be chosen is at least this
 // Falling order of eight words that rise and fall, or fall and rise.
 __device__ __forceinline__ void sort_bitonic8(uint32_t (&l)[8]) {
 #pragma unroll
@@ -576,8 +582,10 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
         else if (c[i] != -INFINITY) size = fmaxf(size, fmaxf(s, fabsf(c[i])));
       }
       again |= c[i] != c[i];  // NaN is left to the second look
-      const uint32_t k = order_key32(bias || !BY_SCORE ? c[i] : x[i], dead || c[i] == -INFINITY);
-      l[i] = k < IDX ? 0 : (k & ~(uint32_t)(IDX - 1)) | (uint32_t)(IDX - 1 - e);
+      // (-inf maps below WORD_LIVE by itself)
+      float v = bias || !BY_SCORE ? c[i] : x[i];
+      if (BY_SCORE && !bias && c[i] == -INFINITY) v = -INFINITY;
+      l[i] = (plain_key32(v) & ~(uint32_t)(IDX - 1)) | (uint32_t)(IDX - 1 - e);
       if (grouped && e < a.K) cs[e] = c[i];
     }
     float tol = 0.f;
@@ -653,7 +661,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
       if (i == sub) word = top[i];
       if (i == a.top_k - 1) last = top[i];
     }
-    int e = sub < a.top_k && word != 0 ? IDX - 1 - (int)(word & (IDX - 1)) : -1;
+    int e = sub < a.top_k && word >= WORD_LIVE ? IDX - 1 - (int)(word & (IDX - 1)) : -1;
     float v = e >= 0 ? to_f32(row[e]) : 0.f;
     const float b = BY_SCORE && bias && e >= 0 ? bias[e] : 0.f;
     {
@@ -661,7 +669,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
       const uint32_t wn = __shfl_down_sync(0xffffffffu, word, 1);
       const float vn = __shfl_down_sync(0xffffffffu, v, 1), bn = __shfl_down_sync(0xffffffffu, b, 1);
       const uint32_t bits = ~(uint32_t)(IDX - 1);
-      if (sub + 1 < a.top_k && e >= 0 && wn != 0) {
+      if (sub + 1 < a.top_k && e >= 0 && wn >= WORD_LIVE) {
         bool close = (word & bits) == (wn & bits);
         if (BY_SCORE && bias) close |= !(key_value(word & bits) - key_value((wn & bits) | (IDX - 1)) > tol);
         again |= close && !(v == vn && b == bn);
@@ -669,18 +677,20 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
       // the last one chosen and those left over
       const int from = r * LANES + a.top_k - 1;
       const float vl = __shfl_sync(0xffffffffu, v, from), bl = __shfl_sync(0xffffffffu, b, from);
-      const float cut = last ? key_value(last & bits) - tol : INFINITY;
+      const bool scored = BY_SCORE && bias;
+      const float cut = last >= WORD_LIVE ? key_value(last & bits) - tol : INFINITY;
+      // a word less than IDX below the last one: the same bits, or nearly
+      auto near_last = [&](int i) {
+        return last - 1 - l[i] < IDX || (scored && l[i] < last && l[i] >= WORD_LIVE && !(c[i] < cut));
+      };
       bool close = false;
 #pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        close |= l[i] != 0 && l[i] < last &&
-                 ((l[i] & bits) == (last & bits) || (BY_SCORE && bias && !(c[i] < cut)));
-      if (close) {
+      for (int i = 0; i < NPL; ++i) close |= near_last(i);
+      if (close && last >= WORD_LIVE) {
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
-          if (l[i] != 0 && l[i] < last &&
-              ((l[i] & bits) == (last & bits) || (BY_SCORE && bias && !(c[i] < cut))))
-            again |= !(x[i] == vl && (!BY_SCORE || !bias || bias[sub * NPL + i] == bl));
+          if (near_last(i) && l[i] >= WORD_LIVE)
+            again |= !(x[i] == vl && (!scored || bias[sub * NPL + i] == bl));
       }
     }
     again = row_any(again) && t < n;
