@@ -61,7 +61,11 @@ __device__ __forceinline__ uint32_t embed_key(const int64_t *ids, int64_t i, int
   return (uint32_t)n_rows;
 }
 
-// hist[bin][block]: keys of the block's tile by digit.  FIRST reads the ids,
+// With up to 64 tiles a scatter block adds up the tiles before its own itself,
+// from hist[block][bin]; with more, k_sort_scan does, in hist[bin][block].
+__host__ __device__ inline bool sort_direct(int nb) { return nb <= 64; }
+
+// hist: keys of the block's tile by digit.  FIRST reads the ids,
 // clears the status word (the scatter records bad ids) and has its blocks
 // from nb on zero the table's gradient.
 template <bool FIRST>
@@ -99,7 +103,9 @@ __global__ void k_sort_hist(int64_t n, const int64_t *__restrict__ ids, int64_t 
     if (d < SORT_BINS && (threadIdx.x & 31) == __ffs(same) - 1) atomicAdd(&h[d], __popc(same));
   }
   __syncthreads();
-  hist[(int64_t)threadIdx.x * nb + blockIdx.x] = h[threadIdx.x];
+  const int64_t at = sort_direct(nb) ? (int64_t)blockIdx.x * SORT_BINS + threadIdx.x
+                                     : (int64_t)threadIdx.x * nb + blockIdx.x;
+  hist[at] = h[threadIdx.x];
 }
 
 // Block-wide exclusive scan of one int per thread (256 threads); *total.
@@ -166,7 +172,19 @@ __global__ void __launch_bounds__(SORT_THREADS)
     }
     d[r] = i < n ? (k[r] >> shift) & mask : SORT_BINS;
   }
-  const int before = hist[(int64_t)tid * gridDim.x + blockIdx.x], total = totals[tid];
+  int before, total;
+  if (sort_direct(gridDim.x)) {
+    before = total = 0;
+#pragma unroll 8
+    for (int b = 0; b < (int)gridDim.x; ++b) {
+      const int v = hist[b * SORT_BINS + tid];
+      total += v;
+      if (b < (int)blockIdx.x) before += v;
+    }
+  } else {
+    before = hist[(int64_t)tid * gridDim.x + blockIdx.x];
+    total = totals[tid];
+  }
 #pragma unroll
   for (int i = 0; i < SORT_WARPS; ++i) cnt[i][tid] = 0;
   if (tid < SORT_WARPS) cnt[tid][SORT_BINS] = 0;
@@ -581,8 +599,10 @@ so2_status embed_grad(const so2conv_embed_desc *d, int64_t n, const int64_t *ids
       k_sort_hist<false><<<p.nb, SORT_THREADS, 0, s>>>(n, nullptr, 0, 0, ki, shift, mask, p.nb, hist,
                                                        nullptr, 0, st);
     MODEL_CKL();
-    k_sort_scan<<<SORT_BINS, SORT_THREADS, 0, s>>>(p.nb, hist, totals);
-    MODEL_CKL();
+    if (!sort_direct(p.nb)) {
+      k_sort_scan<<<SORT_BINS, SORT_THREADS, 0, s>>>(p.nb, hist, totals);
+      MODEL_CKL();
+    }
     if (q == 0)
       k_sort_scatter<true><<<p.nb, SORT_THREADS, 0, s>>>(n, ids, d->n_rows, d->pad_id, nullptr,
                                                          nullptr, shift, mask, hist, totals, ko, po, st);
