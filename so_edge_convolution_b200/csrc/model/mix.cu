@@ -770,6 +770,19 @@ so2_status mix_back_slots(const so2conv_mix_desc *d, int64_t T, const MixPlan &p
   return mix_back_slots<128, TE>(d, T, p, x, weights, index, offsets, list, grad, ge, part, s);
 }
 
+template <typename TE>
+so2_status mix_tc_back(const so2conv_mix_desc *d, int T, int blocks, const void *experts,
+                       const float *weights, const float *grad, float *ge, float *part,
+                       DevStatus *st, cudaStream_t s) {
+  constexpr int smem = mixbk_smem<TE>();
+  MODEL_CK(cudaFuncSetAttribute(k_mix_tc_back<TE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  k_mix_tc_back<TE><<<blocks, MIXBK_THREADS, smem, s>>>(T, d->n_experts, d->n_weights, weights,
+                                                        static_cast<const TE *>(experts), grad, ge,
+                                                        part, st);
+  MODEL_CKL();
+  return SO2_OK;
+}
+
 template <bool VEC, typename TE>
 so2_status mix_dots(const so2conv_mix_desc *d, int64_t n_systems, const MixPlan &p,
                     const void *experts, const int32_t *index, const float *grad, float *part,
@@ -861,7 +874,6 @@ so2_status so2conv_mix_experts_backward(const so2conv_mix_desc *d, int64_t n_sys
   const bool vec = n % 4 == 0 && aligned_to(experts, 4 * es) && aligned_to(grad_out, 16) &&
                    aligned_to(grad_experts, 16);
   if (vec && p.cols) {
-    if (!grad_experts && !grad_weights) return SO2_OK;
     float *part = grad_weights ? ws_at<float>(ws, p.part) : nullptr;
     r = d->expert_dtype == SO2_F32
             ? mix_back_slots<float>(d, n_systems, p, experts, weights, index, offsets, list, grad_out,
@@ -872,6 +884,24 @@ so2_status so2conv_mix_experts_backward(const so2conv_mix_desc *d, int64_t n_sys
     if (grad_weights) {
       k_mix_dots_join<<<(unsigned)ceil_div(slots, 32), 1024, 0, s>>>(
           slots, K, k, index, false, slots, p.splits, part, grad_weights);
+      MODEL_CKL();
+    }
+    return SO2_OK;
+  }
+  if (!grad_experts && !grad_weights) return SO2_OK;
+  if (!index && vec && n_systems <= MIXBK_T && K <= MIXBK_E && n_systems * K >= MIX_TC_FROM) {
+    float *part = grad_weights ? ws_at<float>(ws, p.part) : nullptr;
+    const int64_t tiles = ceil_div(n, MIXTC_COLS);
+    const int blocks = (int)(tiles < MODEL_SMS ? tiles : MODEL_SMS);  // never over the plan's splits
+    r = d->expert_dtype == SO2_F32
+            ? mix_tc_back<float>(d, (int)n_systems, blocks, experts, weights, grad_out, grad_experts,
+                                 part, st, s)
+            : mix_tc_back<__nv_bfloat16>(d, (int)n_systems, blocks, experts, weights, grad_out,
+                                         grad_experts, part, st, s);
+    if (r != SO2_OK) return r;
+    if (grad_weights) {
+      k_mix_dots_join<<<(unsigned)ceil_div(slots, 32), 1024, 0, s>>>(
+          slots, K, k, nullptr, true, n_systems * K, blocks, part, grad_weights);
       MODEL_CKL();
     }
     return SO2_OK;

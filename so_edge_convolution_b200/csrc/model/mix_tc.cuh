@@ -281,4 +281,281 @@ __global__ void __launch_bounds__(MIXTC_THREADS, 2)
   if (w == 0) tmem_dealloc(tmem, 2 * N);
 }
 
+// ---- both gradients from one split of grad_out -------------------------------------
+// For up to 64 systems and 32 experts.  Of each tile of 128 columns the three
+// parts of G (grad_out) and of the experts W are formed once and serve two
+// products: the experts' gradient, D[column, e] = sum_t G[t, column] a[t, e],
+// which reads G's rows MN-major, and the routing weights', D2[t, e] = sum over
+// the columns of G[t, .] W[e, .], which reads the same bytes K-major (a
+// 128-byte row of 64 columns is a row of either).  The parts of a and of W lie
+// side by side as up to 96 columns of one operand, so each part of G is read
+// once per product: hi [hi mid lo], mid [hi mid], lo [hi], three accumulator
+// ranges that the epilogue adds.  D2 is taken out of tensor memory after each
+// tile and added up in registers, a tile's 128 columns at a time.  Shared
+// memory bounds it (copies in, parts out, operand reads).
+// (The MMAs of D2 are 128 rows high; rows 64.. read what follows G's part in
+// shared memory and are not looked at.)
+// Sixteen warps copy, split and finish; a seventeenth only issues the MMAs (36 a
+// tile: with one of the sixteen doing that, the others waited for it at the
+// tile's barrier).
+constexpr int MIXBK_WORKERS = 512, MIXBK_THREADS = MIXBK_WORKERS + 32, MIXBK_T = 64, MIXBK_E = 32;
+constexpr int MIXBK_G = 3 * MIXBK_T * 256;  // G's parts, bytes
+template <typename TE> constexpr int mixbk_w() { return mixtc_parts<TE>() * MIXBK_E * 256; }
+template <typename TE> constexpr int mixbk_raw() { return (MIXBK_T * 4 + MIXBK_E * (int)sizeof(TE)) * MIXTC_COLS; }
+template <typename TE> constexpr int mixbk_smem() {
+  return 1024 + 2 * (MIXBK_G + mixbk_w<TE>()) + 2 * MIXBK_T * 128 + mixbk_raw<TE>() +
+         MIXBK_T * MIXBK_E * 4 + 64;
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// Eight columns of an accumulator of RANGES ranges of 32, added up.
+template <int RANGES>
+__device__ __forceinline__ void tmem_sum8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  tmem_ld8(taddr, r);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[j]);
+#pragma unroll
+  for (int q = 1; q < RANGES; ++q) {
+    tmem_ld8(taddr + 32 * q, r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(r[j]);
+  }
+}
+
+// ge [K][n] and part[block][t][e]; NULL leaves one out (the other is the same).
+template <typename TE>
+__global__ void __launch_bounds__(MIXBK_THREADS, 1)
+    k_mix_tc_back(int T, int K, int64_t n, const float *__restrict__ weights,
+                  const TE *__restrict__ experts, const float *__restrict__ grad,
+                  float *__restrict__ ge, float *__restrict__ part, DevStatus *st) {
+  extern __shared__ uint8_t raw[];
+  constexpr int WPARTS = mixtc_parts<TE>(), BUF = MIXBK_G + mixbk_w<TE>();
+  constexpr int GPART = MIXBK_T * 256, WCHUNK = WPARTS * MIXBK_E * 128, QW = 4 * (int)sizeof(TE);
+  uint8_t *planes = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *m_smem = planes + 2 * BUF;              // [2 chunks][64 t][hi mid | lo]
+  uint8_t *ring = m_smem + 2 * MIXBK_T * 128;      // a thread's own: four quads of G, two of W
+  float *extra = reinterpret_cast<float *>(ring + mixbk_raw<TE>());  // [64][32] of tiles done with FMAs
+  uint64_t *bar = reinterpret_cast<uint64_t *>(extra + MIXBK_T * MIXBK_E);  // [2]
+  uint32_t *slot = reinterpret_cast<uint32_t *>(bar + 2);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    mbar_init(bar + 1, 1);
+    fence_mbar_init();
+  }
+  if (w == 0) {
+    tmem_alloc(slot, 512);
+    tmem_relinquish();
+  }
+  for (int i = tid; i < MIXBK_T * MIXBK_E; i += MIXBK_THREADS) extra[i] = 0.f;
+  float bad = 0.f;
+  for (int i = tid; i < MIXBK_T * MIXBK_E / 2; i += MIXBK_THREADS) {
+    const int t = i / (MIXBK_E / 2), e = i % (MIXBK_E / 2) * 2;
+    const float v0 = t < T && e < K ? weights[t * K + e] : 0.f;
+    const float v1 = t < T && e + 1 < K ? weights[t * K + e + 1] : 0.f;
+    uint32_t p[3];
+    split3(v0, v1, p[0], p[1], p[2], bad);
+    auto put = [&](int chunk, int r, uint32_t v) {  // columns r, r + 1 of a chunk's row t
+      *reinterpret_cast<uint32_t *>(m_smem + chunk * (MIXBK_T * 128) + t * 128 +
+                                    ((((r >> 3) ^ t) & 7) << 4) + (r & 7) * 2) = v;
+    };
+    put(0, e, p[0]);
+    put(0, 32 + e, p[1]);
+    put(1, e, p[2]);
+    put(1, 32 + e, 0);
+  }
+  const bool bad_m = __syncthreads_or(bad != bad);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+
+  const int64_t tiles = (n + MIXTC_COLS - 1) / MIXTC_COLS;
+  const int64_t mine = blockIdx.x < tiles ? (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+  uint8_t *const own_g = ring + tid * 16, *const own_w = ring + 4 * MIXBK_WORKERS * 16 + tid * QW;
+  auto copy = [&](int64_t i) {  // the block's i-th tile: rows w, w + 16, ..., four columns a lane
+    if (i < mine) {
+      const int64_t c = (blockIdx.x + i * gridDim.x) * MIXTC_COLS + lane * 4;
+      const float *g = grad + w * n + c;
+      const TE *x = experts + w * n + c;
+#pragma unroll
+      for (int k = 0; k < 4; ++k, g += 16 * n) {
+        const bool on = w + 16 * k < T && c < n;
+        copy_async_or_zero<16>(own_g + k * MIXBK_WORKERS * 16, on ? g : grad, on);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k, x += 16 * n) {
+        const bool on = w + 16 * k < K && c < n;
+        copy_async_or_zero<QW>(own_w + k * MIXBK_WORKERS * QW, on ? x : experts, on);
+      }
+    }
+    copy_commit();
+  };
+  const int swz = ((((lane & 15) >> 1) ^ (w & 7)) << 4) + (lane & 1) * 8;
+  const int put_g = (lane >> 4) * (MIXBK_T * 128) + w * 128 + swz;
+  const int put_w = MIXBK_G + (lane >> 4) * WCHUNK + w * 128 + swz;
+  const bool worker = w < 16;
+  const int q = w & 3, e0 = (w >> 2) * 8;  // of the epilogues: tensor memory lanes 32 q.., eight experts
+  float dot[8] = {};
+  auto done = [&](int64_t i) { return mbar_wait(bar + (i & 1), (uint32_t)(i >> 1) & 1, st); };
+  auto finish = [&](int64_t i, bool odd) {
+    const int64_t c0 = (blockIdx.x + i * gridDim.x) * MIXTC_COLS, c = c0 + q * 32 + lane;
+    const uint32_t from = tmem + ((uint32_t)q << 21) + (uint32_t)(i & 1) * 96 + e0;
+    float v[8];
+    if (!ge) {
+    } else if (odd || bad_m) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+      if (c < n)
+        for (int t = 0; t < T; ++t) {
+          const float g = grad[t * n + c];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (e0 + j < K) v[j] = fmaf(weights[t * K + e0 + j], g, v[j]);
+        }
+    } else {
+      tmem_sum8<3>(from, v);
+    }
+    if (ge && c < n) {
+      float *to = ge + e0 * n + c;
+#pragma unroll
+      for (int j = 0; j < 8; ++j, to += n)
+        if (e0 + j < K) *to = v[j];
+    }
+    if (!part) return;
+    if (odd) {  // four (t, e) a thread, its own
+      const int64_t c1 = c0 + MIXTC_COLS < n ? c0 + MIXTC_COLS : n;
+      for (int k = tid * 4; k < tid * 4 + 4; ++k) {
+        const int t = k / MIXBK_E, e = k % MIXBK_E;
+        if (t >= T || e >= K) continue;
+        float s = 0.f;
+        for (int64_t x = c0; x < c1; ++x) s = fmaf(grad[t * n + x], to_f32(experts[e * n + x]), s);
+        extra[k] += s;
+      }
+    } else if (q < 2) {
+      tmem_sum8<WPARTS>(from + 192, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dot[j] += v[j];
+    }
+  };
+
+  bool ok = true, odd_now = false, odd_last = false;
+  if (worker) copy(0);
+  for (int64_t i = 0; i < mine; ++i) {
+    uint8_t *buf = planes + (int)(i & 1) * BUF;
+    float odd = 0.f;
+    if (worker) {
+      copy_wait<0>();
+      if (i > 1) ok = ok && done(i - 2);  // the MMAs that read this buffer
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = *reinterpret_cast<const float4 *>(own_g + k * MIXBK_WORKERS * 16);
+        uint2 h, m, l;
+        split3(v.x, v.y, h.x, m.x, l.x, odd);
+        split3(v.z, v.w, h.y, m.y, l.y, odd);
+        uint8_t *to = buf + put_g + k * 16 * 128;
+        *reinterpret_cast<uint2 *>(to) = h;
+        *reinterpret_cast<uint2 *>(to + GPART) = m;
+        *reinterpret_cast<uint2 *>(to + 2 * GPART) = l;
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint8_t *to = buf + put_w + k * 16 * 128;
+        if constexpr (WPARTS == 1) {
+          const uint2 v = *reinterpret_cast<const uint2 *>(own_w + k * MIXBK_WORKERS * QW);
+          odd = fmaf(__uint_as_float(v.x << 16), 0.f, fmaf(__uint_as_float(v.x & 0xffff0000u), 0.f, odd));
+          odd = fmaf(__uint_as_float(v.y << 16), 0.f, fmaf(__uint_as_float(v.y & 0xffff0000u), 0.f, odd));
+          *reinterpret_cast<uint2 *>(to) = v;
+        } else {
+          const float4 v = *reinterpret_cast<const float4 *>(own_w + k * MIXBK_WORKERS * QW);
+          uint2 h, m, l;
+          split3(v.x, v.y, h.x, m.x, l.x, odd);
+          split3(v.z, v.w, h.y, m.y, l.y, odd);
+          *reinterpret_cast<uint2 *>(to) = h;
+          *reinterpret_cast<uint2 *>(to + MIXBK_E * 128) = m;
+          *reinterpret_cast<uint2 *>(to + 2 * MIXBK_E * 128) = l;
+        }
+      }
+      copy(i + 1);  // (what this thread read is in registers by now)
+      fence_async_shared();
+      tc_fence_before();
+    }
+    odd_last = odd_now;
+    odd_now = false;
+    if (__syncthreads_or(odd != odd || !ok)) {
+      if (__syncthreads_or(!ok)) {
+        ok = false;
+        break;
+      }
+      odd_now = true;
+    }
+    if (tid == MIXBK_WORKERS) {
+      tc_fence_after();
+      const uint32_t g0 = smem_u32(buf), w0 = g0 + MIXBK_G, m0 = smem_u32(m_smem);
+      const uint32_t d = tmem + (uint32_t)(i & 1) * 96, d2 = d + 192;
+      constexpr int NG[3] = {96, 64, 32};  // parts of a that a part of G meets, as columns
+      constexpr int NW[3] = {32 * WPARTS, WPARTS == 1 ? 32 : 64, 32};
+      if (ge) {
+        const uint64_t b = sdesc_mn_sw128(m0, MIXBK_T * 128);
+#pragma unroll
+        for (int pg = 0; pg < 3; ++pg) {
+          const uint64_t a = sdesc_mn_sw128(g0 + pg * GPART, MIXBK_T * 128);
+#pragma unroll
+          for (int kk = 0; kk < MIXBK_T / 16; ++kk)
+            umma_bf16(d, a + kk * 128, b + kk * 128, idesc_bf16_f32(128, NG[pg], true), (pg | kk) != 0);
+        }
+      }
+      if (part) {
+#pragma unroll
+        for (int pg = 0; pg < 3; ++pg)
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch) {
+            const uint64_t a = sdesc_k_sw128(g0 + pg * GPART + ch * (MIXBK_T * 128));
+            const uint64_t b = sdesc_k_sw128(w0 + ch * WCHUNK);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_bf16(d2, a + kk * 2, b + kk * 2, idesc_bf16_f32(128, NW[pg]), (pg | ch | kk) != 0);
+          }
+      }
+      umma_commit(bar + (i & 1));
+    }
+    __syncwarp();
+    if (worker && i > 0) {  // (a wait that gave up shows at the next tile's barrier)
+      ok = __all_sync(0xffffffffu, done(i - 1));
+      tc_fence_after();
+      if (ok) finish(i - 1, odd_last);
+    }
+  }
+  copy_wait<0>();
+  if (mine > 0 && ok) ok = done(mine - 1);  // (every warp: the tensor memory is freed below)
+  if (__syncthreads_or(!ok)) {
+    // a wait gave up (recorded in the status word): give the MMAs in flight a
+    // while longer before their tensor memory is freed
+    const uint64_t since = globaltimer_ns();
+    while (globaltimer_ns() - since < 200000000ull) {
+    }
+  } else if (mine > 0 && worker) {
+    tc_fence_after();
+    finish(mine - 1, odd_now);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (w == 0) tmem_dealloc(tmem, 512);
+  const int t = q * 32 + lane;
+  if (part && worker && q < 2 && t < T)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (e0 + j < K)
+        part[((int64_t)blockIdx.x * T + t) * K + e0 + j] = dot[j] + extra[t * MIXBK_E + e0 + j];
+}
+
 }  // namespace so2

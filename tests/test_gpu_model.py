@@ -366,7 +366,8 @@ def test_mix(T, K, k, n, experts, out):
 @pytest.mark.parametrize("experts,out", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
 @pytest.mark.parametrize("T,K,n", [(16, 32, 128), (33, 31, 4), (64, 64, 1500), (130, 40, 516),
                                    (65, 17, 300), (20, 256, 260), (24, 300, 132), (40, 33, 40004),
-                                   (100, 129, 1028)])
+                                   (100, 129, 1028), (64, 32, 60004), (33, 24, 20000), (64, 12, 516),
+                                   (48, 32, 128 * 148 * 3 + 4)])
 def test_mix_large_dense(T, K, n, experts, out):
     # shapes whose products are matrix products; 40,004 columns make a block take several tiles
     d, e, w, _, G = _mix_case(T, K, None, n, experts, out, seed=T)
@@ -405,6 +406,25 @@ def test_mix_infinities_and_nan_stay_in_their_columns(experts):
     assert torch.isnan(ge[:, 17]).all() and torch.isinf(ge[:, 399]).all()
     ge[:, [17, 399]] = 0
     assert torch.isfinite(ge).all()
+
+
+@pytest.mark.parametrize("experts", ["f32", "bf16"])
+def test_mix_gradients_with_infinities_and_nan(experts):
+    d, e, w, _, G = _mix_case(40, 30, None, 1000, experts, "f32", seed=8)
+    G[1, 900], G[2, 17], e[4, 500], e[5, 200] = -math.inf, math.nan, math.inf, math.nan
+    g = B.mix_experts_backward(d, _dev(e), _dev(w), _dev(G))
+    one = B.mix_experts_backward(d, _dev(e), _dev(w), _dev(G), need=["grad_weights"])
+    assert B.check(DEV) == 0
+    (ge, me), (gw, mw) = M.mix_backward(e, w, G)
+    for name, got, ref, mag in (("grad_experts", g["grad_experts"], ge, 42 * U * me),
+                                ("grad_weights", g["grad_weights"], gw, 1002 * U * mw),
+                                ("grad_weights alone", one["grad_weights"], gw, 1002 * U * mw)):
+        got = got.cpu().double()
+        assert torch.equal(torch.isnan(got), torch.isnan(ref)), name
+        assert torch.equal(torch.isinf(got), torch.isinf(ref)), name
+        inf, fin = torch.isinf(ref), torch.isfinite(ref)
+        assert torch.equal(got[inf], ref[inf]), name
+        assert ((got - ref)[fin].abs() <= mag[fin] + TINY).all(), name
 
 
 def test_mix_bad_index_is_skipped_with_a_status():
