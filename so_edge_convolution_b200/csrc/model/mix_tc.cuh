@@ -501,29 +501,38 @@ __global__ void __launch_bounds__(MIXBK_THREADS, 1)
       tc_fence_after();
       const uint32_t g0 = smem_u32(buf), w0 = g0 + MIXBK_G, m0 = smem_u32(m_smem);
       const uint32_t d = tmem + (uint32_t)(i & 1) * 96, d2 = d + 192;
-      constexpr int NG[3] = {96, 64, 32};  // parts of a that a part of G meets, as columns
+      // Parts of the other operand that a part of G meets, as columns.  The
+      // first high product clears all ranges; the small products follow it and
+      // the other high ones come last, so that few roundings are of full size.
+      constexpr int NG[3] = {96, 64, 32};
       constexpr int NW[3] = {32 * WPARTS, WPARTS == 1 ? 32 : 64, 32};
       if (ge) {
         const uint64_t b = sdesc_mn_sw128(m0, MIXBK_T * 128);
-#pragma unroll
-        for (int pg = 0; pg < 3; ++pg) {
+        auto mma = [&](int pg, int kk, bool more) {
           const uint64_t a = sdesc_mn_sw128(g0 + pg * GPART, MIXBK_T * 128);
+          umma_bf16(d, a + kk * 128, b + kk * 128, idesc_bf16_f32(128, NG[pg], true), more);
+        };
+        mma(0, 0, false);
 #pragma unroll
-          for (int kk = 0; kk < MIXBK_T / 16; ++kk)
-            umma_bf16(d, a + kk * 128, b + kk * 128, idesc_bf16_f32(128, NG[pg], true), (pg | kk) != 0);
-        }
+        for (int pg = 2; pg > 0; --pg)
+#pragma unroll
+          for (int kk = 0; kk < MIXBK_T / 16; ++kk) mma(pg, kk, true);
+#pragma unroll
+        for (int kk = 1; kk < MIXBK_T / 16; ++kk) mma(0, kk, true);
       }
       if (part) {
+        auto mma = [&](int pg, int k8, bool more) {  // 16 of the tile's columns
+          const uint64_t a = sdesc_k_sw128(g0 + pg * GPART + (k8 >> 2) * (MIXBK_T * 128));
+          const uint64_t b = sdesc_k_sw128(w0 + (k8 >> 2) * WCHUNK);
+          umma_bf16(d2, a + (k8 & 3) * 2, b + (k8 & 3) * 2, idesc_bf16_f32(128, NW[pg]), more);
+        };
+        mma(0, 0, false);
 #pragma unroll
-        for (int pg = 0; pg < 3; ++pg)
+        for (int pg = 2; pg > 0; --pg)
 #pragma unroll
-          for (int ch = 0; ch < 2; ++ch) {
-            const uint64_t a = sdesc_k_sw128(g0 + pg * GPART + ch * (MIXBK_T * 128));
-            const uint64_t b = sdesc_k_sw128(w0 + ch * WCHUNK);
+          for (int k8 = 0; k8 < 8; ++k8) mma(pg, k8, true);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_bf16(d2, a + kk * 2, b + kk * 2, idesc_bf16_f32(128, NW[pg]), (pg | ch | kk) != 0);
-          }
+        for (int k8 = 1; k8 < 8; ++k8) mma(0, k8, true);
       }
       umma_commit(bar + (i & 1));
     }
