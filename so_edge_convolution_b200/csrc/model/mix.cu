@@ -22,6 +22,8 @@ constexpr int ROWS_DEPTH = 8;   // copies in flight
 // 1,228,800 f32 columns, FMA / tensor us: 24 x 24 50 / 66, 32 x 16 53 / 64,
 // 32 x 32 82 / 64, 64 x 16 97 / 79, 64 x 64 283 / 125.
 constexpr int MIX_TC_FROM = 768;
+// And from this many products of all (t, e) on, those go in tiles (mix_plan).
+constexpr int MIX_TILES_FROM = 256;
 
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(256)
     float s[4][V];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int e = j0 + u < top_k ? index[t * top_k + j0 + u] : -1;
+      const int e = j0 + u >= top_k ? -1 : index ? index[t * top_k + j0 + u] : j0 + u;
       x[u] = e >= 0 && e < K ? experts + e * n : nullptr;
 #pragma unroll
       for (int v = 0; v < V; ++v) s[u][v] = 0.f;
@@ -602,10 +604,12 @@ MixPlan mix_plan(const so2conv_mix_desc *d, int64_t n_systems, int which) {
     const size_t slots = (size_t)(n_systems * d->top_k);
     p.offsets = ws_take(c, sizeof(int) * (d->n_experts + 1));
     p.list = ws_take(c, sizeof(int) * slots);
-    // The products of all (t, e) in tiles, or of the slots one by one.  Both
-    // gradients of 307,200 bf16 weights, tiles / slots in us: 33 systems, 4 of
-    // 64 experts 121 / 66, 8 of 64 128 / 95, 16 of 64 155 / 137.
-    p.tiles = d->top_k * 2 >= d->n_experts;
+    // The products of all (t, e) in tiles of a fixed size, or of the slots one by
+    // one.  Both gradients of 307,200 bf16 weights, tiles / slots in us: 33
+    // systems, 4 of 64 experts 121 / 66, 8 of 64 128 / 95, 16 of 64 155 / 137.
+    // Of 1,228,800 f32 weights, every expert: 4 x 8 165 / 45, 8 x 16 174 / 103,
+    // 16 x 16 179 / 157, 8 x 32 192 / 254.
+    p.tiles = d->top_k * 2 >= d->n_experts && n_systems * d->n_experts >= MIX_TILES_FROM;
     const int64_t per = p.tiles ? n_systems * d->n_experts : n_systems * d->top_k;  // products
     int64_t want;
     // Up to eight slots a system, and all systems' gradients of at least 128
@@ -613,7 +617,7 @@ MixPlan mix_plan(const so2conv_mix_desc *d, int64_t n_systems, int which) {
     // gradients.  Same case, together / apart in us: 2 of 64 51 / 59, 4 of 64
     // 63 / 66, 8 of 64 86 / 95, but 16 of 64 174 / 137.
     p.cols = 0;
-    if (!p.tiles && n_systems > 0 && d->top_k <= 8 && slots <= BACK_SLOTS && d->n_experts <= BACK_EXPERTS &&
+    if (!p.tiles && n_systems > 0 && d->top_k <= 8 && d->top_k < d->n_experts && slots <= BACK_SLOTS && d->n_experts <= BACK_EXPERTS &&
         d->n_weights % 4 == 0) {
       p.cols = 512;
       while (p.cols >= 128 && n_systems * p.cols * 8 > BACK_BYTES) p.cols /= 2;
@@ -873,7 +877,7 @@ so2_status so2conv_mix_experts_backward(const so2conv_mix_desc *d, int64_t n_sys
   const size_t es = dtype_size(d->expert_dtype);
   const bool vec = n % 4 == 0 && aligned_to(experts, 4 * es) && aligned_to(grad_out, 16) &&
                    aligned_to(grad_experts, 16);
-  if (vec && p.cols) {
+  if (index && vec && p.cols) {
     float *part = grad_weights ? ws_at<float>(ws, p.part) : nullptr;
     r = d->expert_dtype == SO2_F32
             ? mix_back_slots<float>(d, n_systems, p, experts, weights, index, offsets, list, grad_out,
@@ -889,7 +893,9 @@ so2_status so2conv_mix_experts_backward(const so2conv_mix_desc *d, int64_t n_sys
     return SO2_OK;
   }
   if (!grad_experts && !grad_weights) return SO2_OK;
-  if (!index && vec && n_systems <= MIXBK_T && K <= MIXBK_E && n_systems * K >= MIX_TC_FROM) {
+  // (the last case above: 174 us; it costs the same up to 64 x 32, where tiles
+  // and the other kernels take 260)
+  if (!index && vec && n_systems <= MIXBK_T && K <= MIXBK_E && n_systems * K >= MIX_TILES_FROM) {
     float *part = grad_weights ? ws_at<float>(ws, p.part) : nullptr;
     const int64_t tiles = ceil_div(n, MIXTC_COLS);
     const int blocks = (int)(tiles < MODEL_SMS ? tiles : MODEL_SMS);  // never over the plan's splits

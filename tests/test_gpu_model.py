@@ -309,7 +309,8 @@ def test_route_many_rows_and_none():
 
 # ---- mixing ------------------------------------------------------------------------
 MIX = [  # systems, experts, slots (None: every expert in order), weights
-    (6, 40, 12, 260), (9, 30, 16, 132), (97, 50, 3, 132), (40, 20, 2, 1028),
+    (6, 40, 12, 260), (9, 30, 16, 132), (97, 50, 3, 132), (40, 20, 2, 1028), (3, 6, 6, 132),
+    (15, 17, None, 2052), (16, 16, None, 2052), (6, 8, None, 1028), (4, 4, None, 77), (20, 30, 30, 516),
     (1, 1, None, 1), (1, 32, None, 4864), (3, 5, None, 33), (2, 7, 3, 130), (33, 64, 4, 1000),
     (64, 32, None, 2052), (17, 9, 9, 515), (5, 130, None, 257), (70, 3, 2, 96), (130, 40, 5, 260),
     (4, 8, 2, 70001), (9, 128, None, 1028),
