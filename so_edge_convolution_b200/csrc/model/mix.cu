@@ -17,11 +17,13 @@ namespace so2 {
 constexpr int ROWS_THREADS = 128;
 constexpr int ROWS_SC = 32;     // rows of B whose weights are staged together
 constexpr int ROWS_DEPTH = 8;   // copies in flight
-// From this many FMAs a column (R S) on the tensor cores take the product
-// (mix_tc.cuh), whose tiles cost much the same whatever they hold.  Forward of
-// 1,228,800 f32 columns, FMA / tensor us: 24 x 24 50 / 66, 32 x 16 53 / 64,
-// 32 x 32 82 / 64, 64 x 16 97 / 79, 64 x 64 283 / 125.
-constexpr int MIX_TC_FROM = 768;
+// From this many FMAs a column and step of 32 rows of B on, the tensor cores
+// take the product (mix_tc.cuh): a step of theirs costs much the same whatever
+// it holds.  Forward, FMA / tensor us: 1,228,800 f32 columns, R x S = 24 x 24
+// 50 / 66, 32 x 16 53 / 64, 32 x 32 82 / 64, 64 x 16 97 / 79, 64 x 64 283 / 125;
+// 300,000 columns, 8 x 100 23 / 84, 32 x 32 21 / 22, 64 x 32 40 / 29, 30 x 120
+// 60 / 84, 64 x 128 130 / 88.
+constexpr int MIX_TC_FROM = 896;
 // And from this many products of all (t, e) on, those go in tiles (mix_plan).
 constexpr int MIX_TILES_FROM = 256;
 
@@ -702,7 +704,8 @@ template <int V, typename TB, typename TC>
 so2_status launch_rows(int R, int S, int64_t n, const float *M, int64_t mr, int64_t ms, const TB *B,
                        TC *C, DevStatus *st, cudaStream_t s) {
   if constexpr (V == 4) {
-    if (S <= MIXTC_MAX_S && (int64_t)R * S >= MIX_TC_FROM) {
+    const int64_t steps = ceil_div(S, MIXTC_KB);
+    if (S <= MIXTC_MAX_S && R * (int64_t)S >= MIX_TC_FROM * steps) {
       MODEL_CK(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
       for (int r0 = 0; r0 < R; r0 += MIXTC_ROWS) {
         const so2_status e = R - r0 <= 32 ? launch_rows_tc<32>(r0, R, S, n, M, mr, ms, B, C, st, s)

@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(MIXTC_THREADS, 2)
   }
   // M's three parts, MN-major: row s holds 64 r, its 16-byte pieces swizzled by s
   float bad = 0.f;
+#pragma unroll 4  // (the loads of M are what a small product waits for)
   for (int i = tid; i < blocks * KB * 32; i += MIXTC_THREADS) {
     const int s = i >> 5, r = (i & 31) * 2;
     const float v0 = s < S && r < rows ? M[(r0 + r) * mr + s * ms] : 0.f;
