@@ -23,7 +23,7 @@ constexpr int ROWS_DEPTH = 8;   // copies in flight
 // 50 / 66, 32 x 16 53 / 64, 32 x 32 82 / 64, 64 x 16 97 / 79, 64 x 64 283 / 125;
 // 300,000 columns, 8 x 100 23 / 84, 32 x 32 21 / 22, 64 x 32 40 / 29, 30 x 120
 // 60 / 84, 64 x 128 130 / 88.
-constexpr int MIX_TC_FROM = 896;
+constexpr int MIX_TC_FROM = 960;
 // And from this many products of all (t, e) on, those go in tiles (mix_plan).
 constexpr int MIX_TILES_FROM = 256;
 
