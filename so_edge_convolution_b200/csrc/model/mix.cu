@@ -22,7 +22,9 @@ constexpr int ROWS_DEPTH = 8;   // copies in flight
 // it holds.  Forward, FMA / tensor us: 1,228,800 f32 columns, R x S = 24 x 24
 // 50 / 66, 32 x 16 53 / 64, 32 x 32 82 / 64, 64 x 16 97 / 79, 64 x 64 283 / 125;
 // 300,000 columns, 8 x 100 23 / 84, 32 x 32 21 / 22, 64 x 32 40 / 29, 30 x 120
-// 60 / 84, 64 x 128 130 / 88.
+// 60 / 84, 64 x 128 130 / 88.  With few columns the tensor cores would win
+// earlier, which the rule leaves (30 x 120: 4,864 columns 22 / 12, 20,000 22 / 17,
+// 80,000 30 / 31).
 constexpr int MIX_TC_FROM = 960;
 // And from this many products of all (t, e) on, those go in tiles (mix_plan).
 constexpr int MIX_TILES_FROM = 256;

@@ -53,8 +53,9 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t &h, uint32_t &
 
 // A step: 32 rows of B by 128 columns.  Its bytes arrive through a ring of
 // asynchronous copies, MIXTC_RING steps deep, of which a thread reads only what
-// it copied itself (four columns of four rows): with the next step's loads in
-// registers instead, 157 MB arrived at 3 TB/s.
+// it copied itself (four columns of four rows).  With the next step's loads in
+// registers instead it took as long (104 and 105 us at 64 rows x 1,228,800
+// columns); whole steps without a check of each row's bounds brought 85.
 constexpr int MIXTC_KB = 32, MIXTC_RING = 2, MIXTC_PER = MIXTC_KB / 8;
 constexpr int MIXTC_PLANE = MIXTC_KB * 256;  // one part of a step as bf16, bytes
 template <typename TB> constexpr int mixtc_parts() { return sizeof(TB) == 2 ? 1 : 3; }
