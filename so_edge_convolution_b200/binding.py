@@ -8,6 +8,7 @@ does not load, every call raises -- there is no fallback path.
 
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -493,29 +494,33 @@ def _torch_dtype(code):
     return _TORCH_DTYPE[code]
 
 
-_SMALL_WS = {}  # (device index, stream) -> workspace of the calls that need a status word or little more
+_LOCAL = threading.local()  # .small: {(device index, stream): workspace} of this host thread
 _SMALL_WS_BYTES = 4096
 
 
 def _model_ws(need, where, device, ws):
-    """The workspace of one model operator call: the caller's; or, small, one
-    of the current stream's own that is kept; or a new one from torch's
+    """The workspace of one model operator call, which holds it until the
+    library has enqueued its kernels: the caller's; or, small, one that this
+    host thread keeps for the current stream; or a new one from torch's
     allocator, which belongs to the stream, or to the graph being captured.
+    (The interpreter's lock is given up inside the library, so calls of two
+    threads may enqueue their kernels in turn, on one stream too.)
     check() reads the last such call's status."""
     if need == 0:
         raise So2Error(2, where)
     if ws:
-        return ws.get(need)
+        return ws
     if need <= _SMALL_WS_BYTES and not torch.cuda.is_current_stream_capturing():
+        small = _LOCAL.__dict__.setdefault("small", {})
         key = (device.index, _stream(device).value)
-        w = _SMALL_WS.get(key)
+        w = small.get(key)
         if w is None:
-            w = _SMALL_WS[key] = Workspace(device)
+            w = small[key] = Workspace(device)
             w.get(_SMALL_WS_BYTES)
     else:
         w = Workspace(device)
     _MODEL_WS[device] = w
-    return w.get(need)
+    return w
 
 
 def _run(dev, where, call, *args):
@@ -527,6 +532,12 @@ def _run(dev, where, call, *args):
         with torch.cuda.device(dev):
             code = call(*args, _stream(dev))
     _check_call(code, where)
+
+
+def _run_ws(dev, where, need, ws, call, *args):
+    """_run with a workspace of `need` bytes (0: none fits) as the last arguments."""
+    w = _model_ws(need, where, dev, ws)
+    _run(dev, where, call, *args, *w.get(need))
 
 
 def _need(t, name, shape, dtype, device=None):
@@ -591,9 +602,8 @@ def embed_forward(desc, ids, table, out=None, ws=None):
         raise ValueError(f"out must be {dt} of shape {shape} on {dev}")
     ld = _rows_of(out, n, desc.n_comp * desc.channels, "out")
     need = lib.so2conv_embed_workspace_size(ctypes.byref(desc), n, WS_FORWARD)
-    p, nb = _model_ws(need, "embed_workspace_size", dev, ws)
-    _run(dev, "so2conv_embed_forward", lib.so2conv_embed_forward, ctypes.byref(desc), n, _adr(ids),
-         _adr(table), out.data_ptr(), ld, p, nb)
+    _run_ws(dev, "so2conv_embed_forward", need, ws, lib.so2conv_embed_forward, ctypes.byref(desc), n,
+            _adr(ids), _adr(table), out.data_ptr(), ld)
     return out
 
 
@@ -618,9 +628,8 @@ def embed_backward(desc, ids, grad_out, out=None, ws=None):
     ld = desc.channels if n <= 1 else grad_out.stride(0)
     out = _given_out(out, "out", (desc.n_rows, desc.channels), torch.float32, ids)
     need = lib.so2conv_embed_workspace_size(ctypes.byref(desc), n, WS_BACKWARD)
-    p, nb = _model_ws(need, "embed_workspace_size", dev, ws)
-    _run(dev, "so2conv_embed_backward", lib.so2conv_embed_backward, ctypes.byref(desc), n,
-         _adr(ids), grad_out.data_ptr(), ld, _adr(out), p, nb)
+    _run_ws(dev, "so2conv_embed_backward", need, ws, lib.so2conv_embed_backward, ctypes.byref(desc),
+            n, _adr(ids), grad_out.data_ptr(), ld, _adr(out))
     return out
 
 
@@ -683,9 +692,8 @@ def mix_experts_forward(desc, experts, weights, index=None, out=None, ws=None):
     n, dev, experts, weights, index = _mix_inputs(desc, experts, weights, index)
     out = _given_out(out, "out", (n, desc.n_weights), _torch_dtype(desc.out_dtype), experts)
     need = lib.so2conv_mix_workspace_size(ctypes.byref(desc), n, WS_FORWARD)
-    p, nb = _model_ws(need, "mix_workspace_size", dev, ws)
-    _run(dev, "so2conv_mix_experts_forward", lib.so2conv_mix_experts_forward, ctypes.byref(desc), n,
-         _adr(experts), _adr(weights), _adr(index), _adr(out), p, nb)
+    _run_ws(dev, "so2conv_mix_experts_forward", need, ws, lib.so2conv_mix_experts_forward,
+            ctypes.byref(desc), n, _adr(experts), _adr(weights), _adr(index), _adr(out))
     return out
 
 
@@ -701,10 +709,9 @@ def mix_experts_backward(desc, experts, weights, grad_out, index=None, need=None
     shapes = {"grad_experts": (desc.n_experts, desc.n_weights), "grad_weights": (n, desc.top_k)}
     outs = _outputs(names, need, shapes, out, dict(dtype=torch.float32, device=dev))
     size = lib.so2conv_mix_workspace_size(ctypes.byref(desc), n, WS_BACKWARD)
-    p, nb = _model_ws(size, "mix_workspace_size", dev, ws)
-    _run(dev, "so2conv_mix_experts_backward", lib.so2conv_mix_experts_backward, ctypes.byref(desc),
-         n, _adr(experts), _adr(weights), _adr(index), _adr(grad_out),
-         *[_adr(outs[k]) for k in names], p, nb)
+    _run_ws(dev, "so2conv_mix_experts_backward", size, ws, lib.so2conv_mix_experts_backward,
+            ctypes.byref(desc), n, _adr(experts), _adr(weights), _adr(index), _adr(grad_out),
+            *[_adr(outs[k]) for k in names])
     return {k: t for k, t in outs.items() if t is not None}
 
 
