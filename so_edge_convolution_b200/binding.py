@@ -498,6 +498,14 @@ _LOCAL = threading.local()  # .small: {(device index, stream): workspace} of thi
 _SMALL_WS_BYTES = 4096
 
 
+def _capturing(device):
+    """Whether a graph is being captured on the current stream of `device`."""
+    if torch.cuda.current_device() == device.index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _model_ws(need, where, device, ws):
     """The workspace of one model operator call, which holds it until the
     library has enqueued its kernels: the caller's; or, small, one that this
@@ -510,7 +518,7 @@ def _model_ws(need, where, device, ws):
         raise So2Error(2, where)
     if ws:
         return ws
-    if need <= _SMALL_WS_BYTES and not torch.cuda.is_current_stream_capturing():
+    if need <= _SMALL_WS_BYTES and not _capturing(device):
         small = _LOCAL.__dict__.setdefault("small", {})
         key = (device.index, _stream(device).value)
         w = small.get(key)

@@ -83,3 +83,32 @@ def test_a_thread_keeps_its_small_workspace(host):
     _mix_backward()
     _mix_backward()
     assert calls[0][-2].value == calls[1][-2].value
+
+
+def test_capture_is_looked_up_on_the_tensors_device(monkeypatch):
+    # device 1's stream is being captured while device 0 is the current one
+    current = [0]
+
+    class Guard:
+        def __init__(self, device):
+            self.to = device.index
+
+        def __enter__(self):
+            self.was, current[0] = current[0], self.to
+
+        def __exit__(self, *exc):
+            current[0] = self.was
+
+    class Memory(B.Workspace):
+        def get(self, nbytes):
+            return B.ctypes.c_void_p(256), nbytes
+
+    monkeypatch.setattr(B, "Workspace", Memory)
+    monkeypatch.setattr(B, "_MODEL_WS", {})
+    monkeypatch.setattr(B, "_stream", lambda device: B.ctypes.c_void_p(7))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: current[0] == 1)
+    ws = lambda i: B._model_ws(64, "x", torch.device("cuda", i), None)  # noqa: E731
+    assert ws(1) is not ws(1)  # recorded calls never share one
+    assert ws(0) is ws(0) and current == [0]
