@@ -174,12 +174,16 @@ def _check_call(code, where):
         raise So2Error(code, where)
 
 
+_RECORDED = -1  # in place of a stream: a call recorded into a graph, which any stream may replay
+
+
 class Workspace:
     """A reusable device workspace (grown on demand, 256-byte aligned)."""
 
     def __init__(self, device):
         self.device = torch.device(device)
         self.buf = None
+        self.stream = None  # of the last model operator in it, or _RECORDED
 
     def get(self, nbytes):
         if self.buf is None or self.buf.numel() < nbytes + 256:
@@ -318,10 +322,15 @@ def double_backward(desc, x, edge_index, edge_vec, w, w_rad, b_rad, grad_out, gg
 
 def check(device, ws=None):
     """Synchronise and return the device status of the last call (0 = ok): the
-    last one made with `ws`, or without a workspace of its own on `device`."""
+    last one made with `ws`, or without a workspace of its own on `device`, on
+    whatever stream.  Calls that were refused, and calls recorded into a graph
+    without a workspace of their own, are not looked at.  (The workspace of
+    the last call stays allocated for this until the next call.)"""
     w = ws or _MODEL_WS.get(_device(device)) or workspace(device)
     if w.buf is None:
         return 0
+    if w.stream is not None and w.stream != (_stream(device).value or 0):
+        torch.cuda.synchronize(device)
     base = w.buf.data_ptr()
     return int(load().so2conv_check(ctypes.c_void_p(base + (-base) % 256),
                                     _stream(device)))
@@ -512,22 +521,21 @@ def _model_ws(need, where, device, ws):
     host thread keeps for the current stream; or a new one from torch's
     allocator, which belongs to the stream, or to the graph being captured.
     (The interpreter's lock is given up inside the library, so calls of two
-    threads may enqueue their kernels in turn, on one stream too.)
-    check() reads the last such call's status."""
+    threads may enqueue their kernels in turn, on one stream too.)"""
     if need == 0:
         raise So2Error(2, where)
+    stream = _RECORDED if _capturing(device) else _stream(device).value or 0
     if ws:
-        return ws
-    if need <= _SMALL_WS_BYTES and not _capturing(device):
+        w = ws
+    elif need <= _SMALL_WS_BYTES and stream != _RECORDED:
         small = _LOCAL.__dict__.setdefault("small", {})
-        key = (device.index, _stream(device).value)
-        w = small.get(key)
+        w = small.get((device.index, stream))
         if w is None:
-            w = small[key] = Workspace(device)
+            w = small[device.index, stream] = Workspace(device)
             w.get(_SMALL_WS_BYTES)
     else:
         w = Workspace(device)
-    _MODEL_WS[device] = w
+    w.stream = stream
     return w
 
 
@@ -543,9 +551,12 @@ def _run(dev, where, call, *args):
 
 
 def _run_ws(dev, where, need, ws, call, *args):
-    """_run with a workspace of `need` bytes (0: none fits) as the last arguments."""
+    """_run with a workspace of `need` bytes (0: none fits) as the last
+    arguments, whose status check() then reads."""
     w = _model_ws(need, where, dev, ws)
     _run(dev, where, call, *args, *w.get(need))
+    if not ws and w.stream != _RECORDED:
+        _MODEL_WS[dev] = w
 
 
 def _need(t, name, shape, dtype, device=None):

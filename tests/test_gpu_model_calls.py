@@ -1,4 +1,4 @@
-"""Calls of the model operators from several host threads."""
+"""Calls of the model operators from several host threads, and their status."""
 
 import threading
 
@@ -69,3 +69,31 @@ def test_host_threads_on_one_stream(n, tokens):
         return run
     _in_threads([work(k) for k in range(3)])
     assert not wrong
+
+
+def test_status_of_a_call_on_another_stream():
+    side = torch.cuda.Stream()
+    d = B.make_embed_desc(9, 12)
+    ids = torch.tensor([1, 9, 2], device=DEV)  # 9 is no row
+    t, a = torch.ones((9, 12), device=DEV), torch.ones((4096, 4096), device=DEV)
+    own = B.Workspace(DEV)
+    for ws in (None, own):
+        B.embed_forward(d, ids[:1], t, ws=ws)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(50):  # some milliseconds before the call's kernel
+                a @ a
+            B.embed_forward(d, ids, t, ws=ws)
+        assert B.check(DEV, ws=ws) == 5
+    # a refused call leaves the last one's status alone, a recorded one too
+    B.embed_forward(d, ids, t)
+    with pytest.raises(B.So2Error):
+        B.embed_forward(d, ids[1:], t, out=torch.zeros((1, 1, 12), device=DEV).expand(2, 1, 12))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.embed_forward(d, ids, t)
+        B.embed_forward(d, ids, t, ws=own)
+    assert B.check(DEV) == 5 and B.check(DEV) == 0
+    with torch.cuda.stream(side):
+        graph.replay()
+    assert B.check(DEV, ws=own) == 5

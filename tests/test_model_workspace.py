@@ -112,3 +112,41 @@ def test_capture_is_looked_up_on_the_tensors_device(monkeypatch):
     ws = lambda i: B._model_ws(64, "x", torch.device("cuda", i), None)  # noqa: E731
     assert ws(1) is not ws(1)  # recorded calls never share one
     assert ws(0) is ws(0) and current == [0]
+
+
+def test_check_waits_for_the_calls_stream(host, monkeypatch):
+    waited, streams = [], [7]
+    host(1024)
+    lib = Lib(1024)
+    lib.so2conv_check = lambda ws, stream: 0
+    monkeypatch.setattr(B, "load", lambda: lib)
+    monkeypatch.setattr(B, "_device", torch.device)
+    monkeypatch.setattr(B, "_stream", lambda device: B.ctypes.c_void_p(streams[0]))
+    monkeypatch.setattr(torch.cuda, "synchronize", waited.append)
+    _mix_backward()
+    assert B.check("cpu") == 0 and not waited  # the same stream: the library waits for it
+    streams[0] = 0
+    assert B.check("cpu") == 0 and waited == ["cpu"]
+    own = B.Workspace("cpu")
+    d = B.make_mix_desc(3, 8)
+    B.mix_experts_forward(d, torch.zeros(3, 8), torch.zeros(4, 3), ws=own)
+    assert B.check("cpu", ws=own) == 0 and len(waited) == 1
+    streams[0] = 9
+    assert B.check("cpu", ws=own) == 0 and len(waited) == 2
+
+
+def test_check_looks_at_calls_that_ran(host, monkeypatch):
+    def refuse(dev, where, call, *args):
+        raise B.So2Error(1, where)
+
+    host(1 << 20)
+    _mix_backward()
+    last = B._MODEL_WS[torch.device("cpu")]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    _mix_backward()  # recorded: nothing has written its status
+    assert B._MODEL_WS[torch.device("cpu")] is last
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    host(1 << 20, refuse)
+    with pytest.raises(B.So2Error):
+        _mix_backward()
+    assert B._MODEL_WS[torch.device("cpu")] is last
