@@ -526,6 +526,8 @@ def _model_ws(need, where, device, ws):
         raise So2Error(2, where)
     stream = _RECORDED if _capturing(device) else _stream(device).value or 0
     if ws:
+        if _device(ws.device) != device:
+            raise ValueError(f"ws must be on {device}, not {ws.device}")
         w = ws
     elif need <= _SMALL_WS_BYTES and stream != _RECORDED:
         small = _LOCAL.__dict__.setdefault("small", {})

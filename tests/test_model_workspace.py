@@ -150,3 +150,12 @@ def test_check_looks_at_calls_that_ran(host, monkeypatch):
     with pytest.raises(B.So2Error):
         _mix_backward()
     assert B._MODEL_WS[torch.device("cpu")] is last
+
+
+def test_a_workspace_of_another_device_is_refused(host):
+    calls = host(64)
+    for device in ("meta", "cuda:1"):
+        with pytest.raises(ValueError):
+            B.mix_experts_forward(B.make_mix_desc(3, 8), torch.zeros(3, 8), torch.zeros(4, 3),
+                                  ws=B.Workspace(device))
+    assert not calls
