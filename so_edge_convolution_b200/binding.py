@@ -199,7 +199,7 @@ _MODEL_WS = {}  # device -> workspace of the last model operator there, if it ca
 
 
 def workspace(device):
-    key = torch.device(device)
+    key = _device(device)
     if key not in _WS:
         _WS[key] = Workspace(key)
     return _WS[key]

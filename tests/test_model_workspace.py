@@ -159,3 +159,9 @@ def test_a_workspace_of_another_device_is_refused(host):
             B.mix_experts_forward(B.make_mix_desc(3, 8), torch.zeros(3, 8), torch.zeros(4, 3),
                                   ws=B.Workspace(device))
     assert not calls
+
+
+def test_a_device_without_its_index_is_the_current_one(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(B, "_WS", {})
+    assert B.workspace("cuda") is B.workspace("cuda:0")  # so check("cuda") sees the calls on it
