@@ -693,7 +693,7 @@ template <int N, typename TB, typename TC>
 so2_status launch_rows_tc(int r0, int R, int S, int64_t n, const float *M, int64_t mr, int64_t ms,
                           const TB *B, TC *C, DevStatus *st, cudaStream_t s) {
   const int blocks = (S + MIXTC_KB - 1) / MIXTC_KB, smem = mixtc_smem<TB>(blocks);
-  MODEL_CK(cudaFuncSetAttribute(k_mix_tc<N, TB, TC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  if (!allow_smem(k_mix_tc<N, TB, TC>, smem, mixtc_smem<TB>(MIXTC_MAX_S / MIXTC_KB))) return SO2_ERR_CUDA;
   const int64_t tiles = ceil_div(n, MIXTC_COLS);
   const int64_t most = MODEL_SMS * (smem <= 112 * 1024 ? 2 : 1);
   k_mix_tc<N, TB, TC><<<(unsigned)(tiles < most ? tiles : most), MIXTC_THREADS, smem, s>>>(
@@ -757,8 +757,8 @@ so2_status mix_back_slots(const so2conv_mix_desc *d, int64_t T, const MixPlan &p
                           const float *weights, const int32_t *index, const int *offsets,
                           const int *list, const float *grad, float *ge, float *part,
                           cudaStream_t s) {
-  MODEL_CK(cudaFuncSetAttribute(k_mix_back_slots<COLS, TE>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem));
+  constexpr int most = BACK_BYTES + BACK_SLOTS * 20 + (BACK_EXPERTS + 1) * 4;
+  if (!allow_smem(k_mix_back_slots<COLS, TE>, p.smem, most)) return SO2_ERR_CUDA;
   k_mix_back_slots<COLS, TE><<<p.splits, 256, p.smem, s>>>(
       (int)T, d->n_experts, d->top_k, d->n_weights, experts, weights, index, offsets, list, grad, ge,
       part);
@@ -784,7 +784,7 @@ so2_status mix_tc_back(const so2conv_mix_desc *d, int T, int blocks, const void 
                        const float *weights, const float *grad, float *ge, float *part,
                        DevStatus *st, cudaStream_t s) {
   constexpr int smem = mixbk_smem<TE>();
-  MODEL_CK(cudaFuncSetAttribute(k_mix_tc_back<TE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  if (!allow_smem(k_mix_tc_back<TE>, smem, smem)) return SO2_ERR_CUDA;
   k_mix_tc_back<TE><<<blocks, MIXBK_THREADS, smem, s>>>(T, d->n_experts, d->n_weights, weights,
                                                         static_cast<const TE *>(experts), grad, ge,
                                                         part, st);
@@ -800,8 +800,7 @@ so2_status mix_dots(const so2conv_mix_desc *d, int64_t n_systems, const MixPlan 
   if (p.tiles) {
     constexpr int red = 4 * DOT_T * DOT_E * 4;
     constexpr int smem = DOT_STAGES * dot_stage_bytes<TE>() > red ? DOT_STAGES * dot_stage_bytes<TE>() : red;
-    MODEL_CK(cudaFuncSetAttribute(k_mix_dot_tiles<VEC, TE>,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    if (!allow_smem(k_mix_dot_tiles<VEC, TE>, smem, smem)) return SO2_ERR_CUDA;
     const int64_t tiles = ceil_div(n_systems, DOT_T) * ceil_div(d->n_experts, DOT_E);
     k_mix_dot_tiles<VEC, TE><<<dim3(p.splits, (unsigned)tiles), 256, smem, s>>>(
         (int)n_systems, d->n_experts, d->n_weights, x, grad, part);

@@ -22,6 +22,15 @@ extern long long g_model_launches;
 
 constexpr int MODEL_SMS = 148;  // B200
 
+// Shared memory for a launch of `bytes`.  The limit belongs to the kernel and not
+// to the launch, so it is always set to the most that any call takes: calls of
+// several host threads then never lower it under one another.
+template <typename K>
+bool allow_smem(K kernel, int bytes, int most) {
+  return bytes <= 48 * 1024 ||
+         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) == cudaSuccess;
+}
+
 inline bool dtype_ok(int32_t d) { return d == SO2_F32 || d == SO2_BF16; }
 inline size_t dtype_size(int32_t d) { return d == SO2_BF16 ? 2 : 4; }
 inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

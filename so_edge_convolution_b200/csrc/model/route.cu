@@ -132,7 +132,7 @@ constexpr float ROUTE_NEAR = 1.f / (1 << 20);
 // Shared memory per warp, in words of 8 bytes: the chosen experts (i32); by
 // score also K + n_groups 64-bit keys and K 32-bit ranks, and the groups' f32
 // scores and keys, which come before those, fit there.
-__host__ __device__ inline int route_words(int K, int n_groups, int top_k, bool by_score) {
+__host__ __device__ constexpr int route_words(int K, int n_groups, int top_k, bool by_score) {
   return (top_k + 1) / 2 + (by_score ? K + n_groups + (K + 1) / 2 : n_groups > 1 ? (K + n_groups + 1) / 2 : 0);
 }
 
@@ -485,7 +485,7 @@ __device__ __forceinline__ void merge8(uint32_t (&l)[8], const uint32_t (&o)[8])
   sort_bitonic8(l);
 }
 
-__host__ __device__ inline int route_top_words(int K, int n_groups, int rows) {
+__host__ __device__ constexpr int route_top_words(int K, int n_groups, int rows) {
   const int f32s = n_groups > 1 ? (rows * (K + n_groups) + 1) / 2 : 0;
   const int slow = K + n_groups + (K + 1) / 2;  // rank_in_64_bits
   return (f32s > slow ? f32s : slow) + rows * 4;
@@ -1053,9 +1053,8 @@ template <int NPL, bool BY_SCORE, typename T>
 so2_status run_route(const RouteArgs &a, int64_t n, const T *logits, const float *bias,
                      float *weights, int32_t *index, int32_t *counts, cudaStream_t s) {
   const int smem = ROUTE_WARPS * route_words(a.K, a.n_groups, a.top_k, BY_SCORE) * 8 + a.K * 4;
-  if (smem > 48 * 1024)
-    MODEL_CK(cudaFuncSetAttribute(k_route<NPL, BY_SCORE, T>,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  constexpr int KM = 32 * NPL, most = ROUTE_WARPS * route_words(KM, KM, KM, BY_SCORE) * 8 + KM * 4;
+  if (!allow_smem(k_route<NPL, BY_SCORE, T>, smem, most)) return SO2_ERR_CUDA;
   // up to 16 rows one block stores the counts itself, without a clearing launch
   const int grid = n <= 16 ? 1 : route_grid(n);
   if (counts && grid > 1) MODEL_CK(cudaMemsetAsync(counts, 0, sizeof(int32_t) * a.K, s));
@@ -1070,9 +1069,8 @@ so2_status run_route_top(const RouteArgs &a, int64_t n, const T *logits, const f
                          float *weights, int32_t *index, int32_t *counts, cudaStream_t s) {
   constexpr int ROWS = 32 >> SHIFT;
   const int smem = ROUTE_WARPS * route_top_words(a.K, a.n_groups, ROWS) * 8 + a.K * 4;
-  if (smem > 48 * 1024)
-    MODEL_CK(cudaFuncSetAttribute(k_route_top<SHIFT, NPL, BY_SCORE, T>,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  constexpr int KM = NPL << SHIFT;
+  static_assert(ROUTE_WARPS * route_top_words(KM, KM, ROWS) * 8 + KM * 4 <= 48 * 1024, "");
   const int grid = n <= 16 ? 1 : route_grid(ceil_div(n, ROWS));
   if (counts && grid > 1) MODEL_CK(cudaMemsetAsync(counts, 0, sizeof(int32_t) * a.K, s));
   constexpr int V = NPL * sizeof(T) <= 16 ? NPL : 16 / (int)sizeof(T);
@@ -1120,9 +1118,7 @@ so2_status run_route_grad_slots(const RouteArgs &a, int64_t n, const T *logits,
                                 const int32_t *index, const float *gw, float *grad, cudaStream_t s) {
   constexpr int ROWS = 32 >> SHIFT;
   const int smem = ROUTE_WARPS * ((ROWS * a.K + 3) & ~3) * 4;
-  if (smem > 48 * 1024)
-    MODEL_CK(cudaFuncSetAttribute(k_route_grad_slots<SHIFT, T>,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  if (!allow_smem(k_route_grad_slots<SHIFT, T>, smem, ROUTE_WARPS * ROWS * 1024 * 4)) return SO2_ERR_CUDA;
   // a step's rows start on a vector's boundary if one row does, or four of them
   const bool vec = aligned_to(grad, 16) && (ROWS * a.K) % 4 == 0;
   k_route_grad_slots<SHIFT, T><<<route_grid(ceil_div(n, ROWS)), 32 * ROUTE_WARPS, smem, s>>>(

@@ -97,3 +97,24 @@ def test_status_of_a_call_on_another_stream():
     with torch.cuda.stream(side):
         graph.replay()
     assert B.check(DEV, ws=own) == 5
+
+
+def test_host_threads_with_kernels_of_different_sizes():
+    # calls that run the same kernels with more and with less shared memory
+    g = _gen(5)
+    x = torch.randn((16, 1024), generator=g).to(DEV)
+    bias = torch.randn(1024, generator=g).to(DEV)
+    m = torch.randn((256, 64), generator=g).to(DEV)
+    works = []
+    for K, S in ((1024, 256), (1000, 128)):
+        d, md = B.make_route_desc(K, 12), B.make_mix_desc(S, 64)
+        xs, bs = x[:, :K].contiguous(), bias[:K].contiguous()
+        e, w = m[:S].contiguous(), torch.randn((32, S), generator=g).to(DEV)
+
+        def run(d=d, md=md, xs=xs, bs=bs, e=e, w=w):
+            for _ in range(1500):
+                B.route_forward(d, xs, bs)
+                B.mix_experts_forward(md, e, w)
+            torch.cuda.current_stream().synchronize()
+        works.append(run)
+    _in_threads(works)
