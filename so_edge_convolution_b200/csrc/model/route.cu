@@ -6,7 +6,7 @@
 // 32 bits exactly.  With one (or ranks of groups by two scores), c = s + bias
 // is formed in f32 first, and a row in which two scores that meet at a place
 // of the order lie closer than f32 can tell is ranked again in 64 bits.  That
-// is rare (two scores within 2^-20 of each other), so the order of 64 bits
+// is rare (two scores within 40 * 2^-24 of each other), so the order of 64 bits
 // costs what the order of f32 does.
 #include <math.h>
 
@@ -123,11 +123,31 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// How far apart two f32 selection scores of at most this size have to be for
-// their order to hold in 64 bits: s is off by less than 8 of its 2^-24 (the
-// argument's rounding times exp's own falling value, exp, sum and division),
-// c by one more rounding, a group's rank by twice that.
-constexpr float ROUTE_NEAR = 1.f / (1 << 20);
+// How far apart two f32 selection scores of a row have to be for their order to
+// hold in 64 bits, relative to the row's largest score or |c|.  In units of
+// u = 2^-24 of that, with expf within 2 steps (4 u):
+// * each c on its own: the argument's rounding |y| e^-|y| <= 0.4, expf 4, the
+//   division 1, c = s + bias 1: 6.4; a sigmoid's expf 4, sum 1, division 1, c 1: 7;
+// * all softmax scores of a row together, by z: the terms' arguments 4.4 at most
+//   (the solution v of v e^v = 1023 / e), expf 4, sum_exp 14, 1 / z 1: 23.4, which
+//   moves a difference of two by no more than that once.
+// So two of them are right beyond 23.4 + 2 * 6.4 = 36.2, and two groups, whose
+// ranks add two scores and round by 2, beyond 2 * 36.2 + 4 = 76.4 = less than 2 * 40.
+constexpr float ROUTE_NEAR = 40.f / (1 << 24);
+
+// A lane's share of softmax's denominator, in four sums side by side: at most
+// 9 roundings for 32 values, and the 5 of the warp's tree.  (One sum would
+// lose up to 31 terms just below half a step of the first.)
+template <int NPL>
+__device__ __forceinline__ float sum_exp(const float (&x)[NPL], float m0) {
+  constexpr int P = NPL < 4 ? NPL : 4;
+  float z[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) z[i] = expf(x[i] - m0);
+#pragma unroll
+  for (int i = P; i < NPL; ++i) z[i % P] += expf(x[i] - m0);
+  return P == 4 ? (z[0] + z[1]) + (z[P - 2] + z[P - 1]) : P == 2 ? z[0] + z[P - 1] : z[0];
+}
 
 // Shared memory per warp, in words of 8 bytes: the chosen experts (i32); by
 // score also K + n_groups 64-bit keys and K 32-bit ranks, and the groups' f32
@@ -215,10 +235,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
       for (int i = 1; i < NPL; ++i) m0 = fmaxf(m0, x[i]);
       m0 = warp_max(m0);
       if (m0 == -INFINITY) m0 = 0.f;  // a row without any expert
-      z = 0.f;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) z += expf(x[i] - m0);
-      z = warp_sum(z);
+      z = warp_sum(sum_exp(x, m0));
     }
     uint32_t key[NPL];
     float size = 0.f;  // BY_SCORE: the scores' largest magnitude, for what counts as near
@@ -232,7 +249,8 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
         const float s = a.softmax ? expf(x[i] - m0) / z : sigmoid_f(x[i]);
         c = s + (bias && e < a.K ? bias[e] : 0.f);
         again |= !dead && c != c;  // NaN: let 64 bits sort it out
-        if (!dead && c != -INFINITY) size = fmaxf(size, fmaxf(s, fabsf(c)));
+        // (a score counts where the bias takes its expert out too: the others' errors are relative to it)
+        if (!dead) size = fmaxf(size, c == -INFINITY ? s : fmaxf(s, fabsf(c)));
       }
       key[i] = order_key32(bias || !BY_SCORE ? c : x[i], dead);
       if (grouped && e < a.K) cs[e] = dead ? -INFINITY : c;
@@ -559,10 +577,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
       for (int i = 1; i < NPL; ++i) m0 = fmaxf(m0, x[i]);
       m0 = row_max(m0);
       if (m0 == -INFINITY) m0 = 0.f;
-      z = 0.f;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) z += expf(x[i] - m0);
-      z = row_sum(z);
+      z = row_sum(sum_exp(x, m0));
     }
     // words, and by score the scores for a second look at what is near
     uint32_t l[NPL];
@@ -579,7 +594,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
         const float s = a.softmax ? expf(x[i] - m0) * iz : sigmoid_f(x[i]);
         c[i] = s + (bias && e < a.K ? bias[e] : 0.f);
         if (dead) c[i] = -INFINITY;
-        else if (c[i] != -INFINITY) size = fmaxf(size, fmaxf(s, fabsf(c[i])));
+        else size = fmaxf(size, c[i] == -INFINITY ? s : fmaxf(s, fabsf(c[i])));
       }
       again |= c[i] != c[i];  // NaN is left to the second look
       // (-inf maps below WORD_LIVE by itself)

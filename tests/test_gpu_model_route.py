@@ -1,0 +1,59 @@
+"""Routing on the GPU where f32 scores alone would choose another expert than the
+definition, and over many rows."""
+
+import math
+
+import pytest
+import torch
+
+from oracle import model as M
+from so_edge_convolution_b200 import binding as B
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from so_edge_convolution_b200 import build
+    build.build()
+    B.load()
+    torch.cuda.init()
+
+
+def _index(x, bias, **kw):
+    """The chosen experts, after a check against the definition."""
+    d = B.make_route_desc(x.shape[1], **kw)
+    _, i, _ = B.route_forward(d, x.to(DEV), bias.to(DEV))
+    _, ri, _ = M.route_forward(x, bias, **kw)
+    assert torch.equal(i.cpu().long(), ri)
+    return ri
+
+
+@pytest.mark.parametrize("K,per_lane,lanes", [(128, 16, 8), (256, 16, 16), (512, 16, 32), (1024, 32, 32)])
+def test_scores_that_a_sum_rounds_away(K, per_lane, lanes):
+    # beside one expert's 1, exponentials just below half a step of it: each is lost
+    # in an f32 sum that meets it alone, together they are 18 to 31 halves of a step
+    x = torch.full((1, K), -math.inf)
+    x[0, 1:per_lane] = -16.65
+    x[0, [per_lane << i for i in range(int(math.log2(lanes)))]] = -16.65
+    x[0, 0], x[0, K - 1] = 0.0, -60.0
+    bias = torch.zeros(K)
+    bias[K - 1] = 1.0 - 17 * U  # above the first one's score, which f32 takes for 1
+    assert _index(x, bias, top_k=1).item() == K - 1
+    assert _index(x, bias, top_k=2).tolist() == [[K - 1, 0]]
+    assert _index(x, bias, top_k=9)[0, :2].tolist() == [K - 1, 0]
+    bias[K - 1] = 1.0 - 40 * U  # below it
+    assert _index(x, bias, top_k=1).item() == 0
+
+
+@pytest.mark.parametrize("K,k", [(40, 1), (40, 10), (600, 2)])
+def test_scores_far_below_an_expert_that_the_bias_takes_out(K, k):
+    # -80 - 3.75e-6 rounds to -80, half a step or 63 * 2^-24 of the score: small beside
+    # the largest score, large beside those that are left
+    x, bias = torch.full((1, K), -200.0), torch.zeros(K)
+    x[0, 0], bias[0] = 3.75e-6, -math.inf
+    x[0, 1] = -80.0
+    bias[2] = math.exp(-80.0 - 3.75e-6) * (1 + 5 * U)
+    assert _index(x, bias, top_k=k)[0, 0] == 2
