@@ -134,6 +134,9 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // So two of them are right beyond 23.4 + 2 * 6.4 = 36.2, and two groups, whose
 // ranks add two scores and round by 2, beyond 2 * 36.2 + 4 = 76.4 = less than 2 * 40.
 constexpr float ROUTE_NEAR = 40.f / (1 << 24);
+// And in absolute terms, for scores that f32 loses: a sigmoid is 0 where e^-x
+// overflows, below 2^-128, and denormal ones keep steps of 2^-149.
+constexpr float ROUTE_LEAST = 1.f / (1ull << 63) / (1ull << 62);  // 2^-125
 
 // A lane's share of softmax's denominator, in four sums side by side: at most
 // 9 roundings for 32 values, and the 5 of the warp's tree.  (One sum would
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
       if (grouped && e < a.K) cs[e] = dead ? -INFINITY : c;
     }
     float tol = 0.f;
-    if (BY_SCORE) tol = warp_max(size) * ROUTE_NEAR;
+    if (BY_SCORE) tol = warp_max(size) * ROUTE_NEAR + ROUTE_LEAST;
     if (grouped) {
       __syncwarp();
       uint32_t *gk = reinterpret_cast<uint32_t *>(cs + a.K);
@@ -604,7 +607,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
       if (grouped && e < a.K) cs[e] = c[i];
     }
     float tol = 0.f;
-    if (BY_SCORE) tol = row_max(size) * ROUTE_NEAR;
+    if (BY_SCORE) tol = row_max(size) * ROUTE_NEAR + ROUTE_LEAST;
     if (grouped) {
       __syncwarp();
       uint32_t *gk = reinterpret_cast<uint32_t *>(cs + a.K);

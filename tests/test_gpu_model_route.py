@@ -57,3 +57,14 @@ def test_scores_far_below_an_expert_that_the_bias_takes_out(K, k):
     x[0, 1] = -80.0
     bias[2] = math.exp(-80.0 - 3.75e-6) * (1 + 5 * U)
     assert _index(x, bias, top_k=k)[0, 0] == 2
+
+
+@pytest.mark.parametrize("K,k", [(40, 1), (40, 10), (600, 2)])
+def test_sigmoids_that_vanish_beside_tiny_biases(K, k):
+    # e^-89 is 2.2e-39, but e^89 overflows f32: the score is 0 there
+    x, bias = torch.full((1, K), -200.0), torch.zeros(K)
+    x[0, 3] = -89.0
+    bias[1] = 1e-39
+    assert _index(x, bias, top_k=k, score="sigmoid")[0, 0] == 3
+    bias[1] = 3e-39
+    assert _index(x, bias, top_k=k, score="sigmoid")[0, 0] == 1
