@@ -68,3 +68,53 @@ def test_sigmoids_that_vanish_beside_tiny_biases(K, k):
     assert _index(x, bias, top_k=k, score="sigmoid")[0, 0] == 3
     bias[1] = 3e-39
     assert _index(x, bias, top_k=k, score="sigmoid")[0, 0] == 1
+
+
+# Many rows: every row's result is its own, so rows that repeat 97 others give the
+# bits of a call on those, which is checked against the definition.  A grid has
+# 9,472 warps at most, of one to eight rows each; every case takes several steps.
+@pytest.mark.parametrize("n,K,kw", [
+    (30001, 40, dict(top_k=12, renormalise=True)),                    # a warp a row, by logit
+    (20003, 600, dict(top_k=3, score="sigmoid")),
+    (30001, 70, dict(top_k=70)),                                      # nothing to select
+    (90001, 40, dict(top_k=12, n_groups=8, top_groups=4, group_top=2)),
+    (170003, 24, dict(top_k=4, renormalise=True)),                    # eight lanes a row
+    (90001, 60, dict(top_k=7, score="sigmoid", renormalise=True, n_groups=5, top_groups=2,
+                     group_top=2)),
+    (50001, 200, dict(top_k=8)),                                      # sixteen lanes a row
+    (170003, 30, dict(top_k=30, score="sigmoid", renormalise=True)),
+    (30001, 64, dict(top_k=40, score="sigmoid", renormalise=True)),
+])
+@pytest.mark.parametrize("biased", [False, True])
+def test_many_rows(n, K, kw, biased):
+    g = torch.Generator().manual_seed(K)
+    x = torch.randn((97, K), generator=g)
+    x[torch.rand((97, K), generator=g) < 0.1] = -math.inf
+    x[5] = -math.inf
+    bias = (torch.randn(K, generator=g) * 0.2).to(DEV) if biased else None
+    gw = torch.randn((97, kw["top_k"]), generator=g)
+    d = B.make_route_desc(K, **kw)
+    few = [x.to(DEV), gw.to(DEV)]
+    at = torch.arange(n, device=DEV) % 97
+    many = [t[at].contiguous() for t in few]
+    res = []
+    for xs, gs in (few, many):
+        w, i, c = B.route_forward(d, xs, bias)
+        res.append((w, i, B.route_backward(d, xs, i, gs), c))
+    _, ri, _ = M.route_forward(x, None if bias is None else bias.cpu(), **kw)
+    assert torch.equal(res[0][1].cpu().long(), ri)
+    for a, b in zip(res[0][:3], res[1][:3]):
+        assert torch.equal(a[at], b)
+    want = torch.bincount(res[1][1][res[1][1] >= 0].long(), minlength=K)
+    assert torch.equal(res[1][3].long(), want)
+
+
+def test_biases_of_the_types_lowest_value():
+    # every other score is near next to them, so each row is ranked in 64 bits
+    g = torch.Generator().manual_seed(3)
+    for K, k in ((64, 6), (300, 9)):
+        x = torch.randn((200, K), generator=g)
+        bias = torch.randn(K, generator=g) * 0.1
+        bias[::3] = torch.finfo(torch.float32).min
+        for kw in (dict(top_k=k), dict(top_k=k, score="sigmoid", n_groups=4, top_groups=2, group_top=2)):
+            _index(x, bias, **kw)
