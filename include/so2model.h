@@ -191,8 +191,8 @@ so2_status so2conv_mix_experts_backward(const so2conv_mix_desc *desc, int64_t n_
  * unit: SO2_DROP_ELEMENT, m = flat index of the element;
  *       SO2_DROP_CHANNEL, m = i * channels + c, one draw for all components of
  *       a channel, which keeps the features equivariant;
- *       SO2_DROP_ROW, m = rows[i] (int64, any value; NULL: i), one draw for a
- *       node, or for all nodes of a system when rows names systems.
+ *       SO2_DROP_ROW, m = rows[i] (its 64 bits taken as unsigned; NULL: i), one
+ *       draw for a node, or for all nodes of a system when rows names systems.
  * A dropped x is not used, so NaN there does not spread.  p = 1 drops all.
  *
  * Limits: 0 <= p <= 1, 1 <= channels <= 65,536, 1 <= n_comp <= 1,024, 0 <= n

@@ -32,8 +32,10 @@ __device__ __forceinline__ uint32_t word_of(uint4 w, int i) {
   return i < 2 ? (i == 0 ? w.x : w.y) : (i == 2 ? w.z : w.w);
 }
 
-// The kernels move x, the residual and out once each; no word is drawn twice,
-// so each kernel is laid out by its unit.
+// The kernels move x, the residual and out once each and are laid out by their
+// unit, so that a thread draws for all that it moves.  (Some words are drawn
+// more than once: by each share of a node's components or of a row, by all
+// lanes of a row's warp, and, where vectors do not fit, for one unit of four.)
 struct DropArgs {
   const uint64_t *rng;
   uint32_t thr;  // p 2^32; p = 1 does not get here as elements or channels

@@ -469,7 +469,9 @@ bool embed_ok(const so2conv_embed_desc *d) {
 // n_rows * n / 32 steps of a warp, and a row's own tokens one eighth of n deep
 // at worst.  Scan / sort in us at 128 channels: 100 rows, 128 tokens 2.3 / 12.3,
 // 2,048 11.5 / 17.9, 4,096 18.1 / 19.3, 8,192 37.4 / 18.4; 2,000 rows, 2,048
-// tokens 9.3 / 26.
+// tokens 9.3 / 26.  Of large tables only the scan was timed, with cold caches
+// and the call: 60,000 x 512, 69 tokens 203 us, where zeroing alone is 26, so
+// the sort is likely the better one there.
 bool embed_scans(const so2conv_embed_desc *d, int64_t n) {
   return n <= 4096 && d->n_rows * n <= (1 << 22);
 }

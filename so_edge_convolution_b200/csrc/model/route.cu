@@ -465,7 +465,11 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
 // two instructions: each lane sorts its words, and SHIFT butterfly steps merge
 // the lanes' best eight.  Keys that differ only in the replaced bits (2^-15 of
 // a value at 256 experts) and, by score, scores that f32 cannot tell apart
-// send the row to rank_in_64_bits: about one row in a hundred.
+// send the row to rank_in_64_bits.  Of 200,000 rows of normally distributed
+// f32 logits the first were 0.07 % (8 of 128) and 0.2 % (8 of 256).  A bias of
+// the type's lowest value makes all scores near beside it, so that every row
+// goes there: 20,000 x 64, top 6, 30 -> 69 us, 20,000 x 128, top 8, 45 -> 171
+// (-inf takes experts out without that).
 __device__ __forceinline__ void exchange(uint32_t &a, uint32_t &b) {
   const uint32_t hi = a > b ? a : b;
   b = a > b ? b : a;

@@ -149,6 +149,25 @@ def test_infinities_in_a_blocks_tiles(tile, dtype):
     assert B.check(DEV) == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_infinite_weights(dtype):
+    # the forward and the experts' gradient are computed apart; the weights' gradient does not see them
+    g = _gen(3)
+    for T, K in ((64, 32), (48, 40), (5, 6)):
+        n = 128 * 148 * 2 + 12
+        e = torch.randint(-4, 5, (K, n), generator=g).double()
+        G = torch.randint(-4, 5, (T, n), generator=g).double()
+        w = torch.randint(-64, 65, (T, K), generator=g).double()
+        e[e == 0], G[G == 0] = 1.0, 1.0
+        w[3, 2] = math.inf
+        d = B.make_mix_desc(K, n, expert_dtype=B.SO2_F32 if dtype == torch.float32 else B.SO2_BF16)
+        args = [t.to(DEV) for t in (e.to(dtype), w.float())]
+        assert torch.equal(B.mix_experts_forward(d, *args).cpu().double(), w @ e)
+        r = B.mix_experts_backward(d, *args, G.float().to(DEV))
+        assert torch.equal(r["grad_experts"].cpu().double(), w.t() @ G)
+        assert torch.equal(r["grad_weights"].cpu().double(), G @ e.t())
+
+
 @pytest.mark.parametrize("T,K,n", [(64, 32, 60004), (33, 24, 20000), (70, 40, 40004), (16, 16, 128 * 148 * 3)])
 def test_error_of_the_weights_gradient(T, K, n):
     # Of random operands.  A rounding of the running sum is at most a step, 2^-23 of it,
