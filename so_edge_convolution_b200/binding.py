@@ -503,7 +503,12 @@ def _torch_dtype(code):
     return _TORCH_DTYPE[code]
 
 
-_LOCAL = threading.local()  # .small: {(device index, stream): workspace} of this host thread
+class _Local(threading.local):
+    def __init__(self):  # in each host thread
+        self.small = {}  # (device index, stream) -> workspace
+
+
+_LOCAL = _Local()
 _SMALL_WS_BYTES = 4096
 
 
@@ -530,10 +535,10 @@ def _model_ws(need, where, device, ws):
             raise ValueError(f"ws must be on {device}, not {ws.device}")
         w = ws
     elif need <= _SMALL_WS_BYTES and stream != _RECORDED:
-        small = _LOCAL.__dict__.setdefault("small", {})
-        w = small.get((device.index, stream))
+        key, small = (device.index, stream), _LOCAL.small
+        w = small.get(key)
         if w is None:
-            w = small[device.index, stream] = Workspace(device)
+            w = small[key] = Workspace(device)
             w.get(_SMALL_WS_BYTES)
     else:
         w = Workspace(device)
