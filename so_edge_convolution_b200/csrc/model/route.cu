@@ -149,7 +149,9 @@ __device__ __forceinline__ float sum_exp(const float (&x)[NPL], float m0) {
   for (int i = 0; i < P; ++i) z[i] = expf(x[i] - m0);
 #pragma unroll
   for (int i = P; i < NPL; ++i) z[i % P] += expf(x[i] - m0);
-  return P == 4 ? (z[0] + z[1]) + (z[P - 2] + z[P - 1]) : P == 2 ? z[0] + z[P - 1] : z[0];
+  if constexpr (P == 1) return z[0];
+  else if constexpr (P == 2) return z[0] + z[1];
+  else return (z[0] + z[1]) + (z[2] + z[3]);
 }
 
 // Shared memory per warp, in words of 8 bytes: the chosen experts (i32); by
